@@ -26,8 +26,8 @@
  *            compute-unit count, and the kernels whose LDS limit has been
  *            raised. It never changes a result. Calls from several host
  *            threads are safe.
- *   Rows     m is the number of activation rows, 1 <= m <= 8. Rows are
- *            independent. Row r's outputs are bit-identical for every m and
+ *   Rows     m is the number of activation rows, 1 <= m <= 8 (the batch calls, the
+ *            row operators and the expert calls say how many). Rows are independent. Row r's outputs are bit-identical for every m and
  *            for every position r in the batch.
  *   Shapes   k is a multiple of 128 (k >= 128); n >= 1. nb = k / 128.
  *   Stream   stream is a hipStream_t passed as void*; 0 is the null stream.
@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define TB_ABI_VERSION 6
+#define TB_ABI_VERSION 7
 #define TB_BLOCK 128
 #define TB_MAX_ROWS 8
 #define TB_MAX_BATCH_ROWS 32
@@ -351,6 +351,127 @@ int tb_ffn_layers(const tb_ffn_weights *layers, int num_layers, const float *x, 
 /* Blocking: synchronises with the device and returns the sticky error word
  * (0 = none) in *error. */
 int tb_ffn_workspace_error(const void *ws, int *error);
+
+/* ---- Around the FFN: residual, norm and int8 rows --------------------------
+ * Element types of the row operators below. */
+enum tb_dtype { TB_F32 = 0, TB_BF16 = 1, TB_F16 = 2 };
+
+/* Residual addition, root-mean-square norm and the rotated int8 copy of the normed rows, in one
+ * pass: what stands before every product of this library in a decoder block.
+ * For every row r, with T the element type:
+ *   s    = round_T(x[r] + res[r])                     (res null: s = x[r])
+ *   f    = 1 / sqrt(mean(s_i^2) + eps)
+ *   u    = H (s * gamma)                              per 128-block, the sums of tb_rotate_quant_i8
+ *   amax = max |u_i|; q_i = rint(u_i * (127/amax))    (fp32, ties to even)
+ *   dq   = amax * fp32(f * fp32(1/(127*sqrt(128))))
+ *   y    = round_T((s * f) * gamma)                   (if y is not null)
+ * q*dq approximates the orthonormal rotation of the normed row, as tb_rotate_quant_i8 on it
+ * would. f scales whole blocks, so it enters dq and not q. A block with amax < 2^-100 has
+ * q = 0, dq = 0. A row of zeros with eps = 0 has f = 0. Any number of rows.
+ *   x, res  T [m][k]; res may be null
+ *   gamma   float [k]
+ *   res_out T [m][k] output: s; may be null, or x or res itself (in place)
+ *   y       T [m][k] output: the normed rows; may be null
+ *   q       int8 [m][k], dq float [m][k/128] outputs
+ * m >= 1, eps >= 0, k/128 <= 15360 (else TB_EUNSUPPORTED). */
+int tb_add_rmsnorm_quant_i8(const void *x, const void *res, const float *gamma, int dtype, int m,
+                            int k, float eps, void *res_out, void *y, int8_t *q, float *dq,
+                            void *stream);
+
+/* ---- Microscaled 4-bit floating point ------------------------------------
+ * For the layers of a ternary model that stay in a 4-bit format. Rows in the OCP
+ * Microscaling format MXFP4: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), one
+ * e8m0 scale 2^(byte - 127) per 32 elements; byte 255 marks a block that is not a number.
+ *   codes  uint8 [rows][k/2]: element i in bits 4 (i % 2) .. + 3 of byte i / 2
+ *   scales uint8 [rows][k/32]
+ * k is a multiple of 128. Any number of rows. */
+typedef struct tb_mxfp4 {
+    const uint8_t *codes;
+    const uint8_t *scales;
+    int32_t n; /* rows */
+    int32_t k;
+} tb_mxfp4;
+
+/* Quantise rows. rotate = 1: of u = fp32(1/sqrt(128)) * H v per 128-block (the sums of
+ * tb_rotate_quant_i8), else of x itself. With amax the largest magnitude of 32 elements, the
+ * scale is 2^(floor(log2 amax) - 2), and each element is divided by it, rounded to the nearest
+ * e2m1 value (ties to the even code) and saturated at 6. A block with amax < 2^-124 is stored
+ * as zeros with scale byte 0; a block that holds a NaN or an infinity (after the rotation) as
+ * codes 0 with scale byte 255.
+ *   x float / bf16 / fp16 [m][k] input, codes and scales outputs */
+int tb_mxfp4_quant(const void *x, int dtype, int m, int k, int rotate, uint8_t *codes,
+                   uint8_t *scales, void *stream);
+
+/* The values that the codes stand for, rounded once to dtype: y [m][k]. NaN where the scale
+ * byte is 255. */
+int tb_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int m, int k, void *y, int dtype,
+                     void *stream);
+
+/* y[r][j] = sum_i A[r][i] W[j][i] of rows A (codes, scales: [m][...] with w->k elements) and a
+ * weight matrix w, summed in fp32 and rounded once to dtype.
+ * The order of the sums depends on (m, n, k) only: the same call gives the same bits. Unlike in
+ * the ternary calls a row's low-order bits may differ between row counts.
+ *   y  dtype [m][w->n] output
+ *   ws workspace of tb_mxfp4_gemm_workspace_bytes(w, m) bytes, 16-byte aligned; null where that
+ *      is 0. It needs no initialisation; calls that share one must not overlap in time.
+ * m >= 1. TB_EINVAL for a workspace that is too small. */
+int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, void *y,
+                  int dtype, void *ws, size_t ws_bytes, void *stream);
+/* Workspace bytes of tb_mxfp4_gemm for m rows (0 also for invalid arguments). */
+size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m);
+
+/* ---- An FFN of experts --------------------------------------------------
+ * Every token goes through topk of a layer's experts, FFNs of one shape in the packed ternary
+ * or sign format. The pairs (token t, choice j), numbered t * topk + j, are sorted by expert; the
+ * products run over each expert's list, of any length from none on; the down product returns to
+ * pair order, where each token's rows are summed.
+ *   tb_moe_plan -> tb_moe_gateup_silu -> tb_moe_down -> tb_moe_combine
+ * Nothing is read back to the host: the lists' lengths stay on the device, and the four calls can
+ * be captured in a graph. Each pair's row has the bits that the calls for one matrix give
+ * (tb_ffn_gateup_silu, tb_ffn_down on its expert's matrices), however many rows an expert has.
+ * tokens, topk >= 1; tokens * topk <= 2^31 - 64; experts <= 65536 (else TB_EUNSUPPORTED). */
+typedef struct tb_experts {
+    const void *codes;      /* [experts][n][k/128][32] ternary or [...][16] sign */
+    const uint16_t *scales; /* [experts][n][k/128], fp16 bits */
+    int32_t experts;
+    int32_t n;
+    int32_t k;
+    int32_t fmt; /* TB_FMT_TERNARY2 or TB_FMT_SIGN1 */
+} tb_experts;
+
+/* Sort the pairs by expert, each expert's in ascending order.
+ *   ids     int32 [tokens][topk] input: the expert of each pair. A pair whose id lies outside
+ *           [0, experts) belongs to no expert: no product is made for it, and tb_moe_combine
+ *           leaves it out. A token may name an expert twice.
+ *   offsets int32 [experts + 1] output: expert e's slots are offsets[e] .. offsets[e+1] - 1
+ *   order   int32 [tokens * topk] output: the pair in each slot; entries from
+ *           offsets[experts] on are left as they were */
+int tb_moe_plan(const int32_t *ids, int tokens, int topk, int experts, int32_t *offsets,
+                int32_t *order, void *stream);
+
+/* h = silu(gate q) * (up q) of every slot's token on its expert, then rotquant(h).
+ *   q   int8 [tokens][wg->k], dq float [tokens][wg->k/128]: rotated int8 rows, one per token
+ *   h   float [tokens * topk][wg->n] workspace (its contents afterwards are unspecified)
+ *   qh  int8 [tokens * topk][wg->n], dqh float [tokens * topk][wg->n/128] outputs, a row per
+ *       slot; rows from offsets[experts] on are left as they were
+ * wg, wu: the same shape and format, n a multiple of 128. */
+int tb_moe_gateup_silu(const tb_experts *wg, const tb_experts *wu, const int8_t *q, const float *dq,
+                       int tokens, int topk, const int32_t *offsets, const int32_t *order, float *h,
+                       int8_t *qh, float *dqh, void *stream);
+
+/* y[order[s]] = down product of slot s, on its expert.
+ *   qh, dqh from tb_moe_gateup_silu; pairs = tokens * topk
+ *   y       float [pairs][wd->n] output, a row per pair; rows of pairs of no expert are left
+ *           as they were */
+int tb_moe_down(const tb_experts *wd, const int8_t *qh, const float *dqh, int pairs,
+                const int32_t *offsets, const int32_t *order, float *y, void *stream);
+
+/* out[t] = sum over j of weights[t][j] * y[t * topk + j], j ascending, in fp32, rounded once to
+ * dtype; pairs of no expert are left out (a token without any gets zeros).
+ *   y float [tokens * topk][n], weights float [tokens][topk], ids as for tb_moe_plan
+ *   out dtype [tokens][n] output */
+int tb_moe_combine(const float *y, const float *weights, const int32_t *ids, int tokens, int topk,
+                   int experts, int n, void *out, int dtype, void *stream);
 
 /* Static description of a status code; never NULL. */
 const char *tb_status_str(int status);

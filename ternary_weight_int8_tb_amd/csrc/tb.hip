@@ -53,6 +53,7 @@
 
 #include "tb.h"
 #include "tb_device.h"
+#include "tb_host.h"
 #include "tb_layers.h"
 #include "tb_lut.h"
 
@@ -1889,13 +1890,11 @@ int device_info(DeviceInfo *out)
     return TB_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-Range range_of(const void *p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+using tbh::aligned16;
+using tbh::dq_unit;
+using tbh::overlaps;
+using tbh::Range;
+using tbh::range_of;
 
 int check_matrix(const tb_matrix *w)
 {
@@ -1924,8 +1923,6 @@ size_t codes_bytes(const tb_matrix *w)
 size_t scales_bytes(const tb_matrix *w) { return (size_t)w->n * (size_t)(w->k / kBlock) * 2; }
 
 int check_rows(int m, int max_rows = TB_MAX_ROWS) { return (m >= 1 && m <= max_rows) ? TB_OK : TB_EINVAL; }
-
-float dq_unit() { return static_cast<float>(1.0 / (127.0 * std::sqrt(128.0))); }
 
 int launch_rotquant(const float *x, int m, int k, int8_t *q, float *dq, hipStream_t stream)
 {

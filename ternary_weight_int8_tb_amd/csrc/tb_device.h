@@ -1,6 +1,6 @@
 // tb_device.h -- device building blocks of the ternary-weight int8 FFN kernels (gfx950).
 //
-// Included by tb.hip only. Every block here is shared by all entry points, so that
+// Included by tb.hip and tb_moe.hip. Every block here is shared by all entry points, so that
 // one weight row is computed the same way whichever kernel runs it. The fold order of a
 // row is fixed by its shape alone: in step i lane cl holds chunk 16 i + cl; the step's
 // partial is the fixed 16-lane row tree of the lanes' terms (scale * dq) * isum; the row's
