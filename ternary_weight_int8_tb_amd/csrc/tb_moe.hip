@@ -148,21 +148,11 @@ struct Core<TB_FMT_TERNARY2> {
     static constexpr int kStep = 8;        // blocks of a step
     static constexpr int kBlockBytes = 32;
     uint2 w;
-    // off: the lane's byte offset in the expert's codes (its row, plus 8 g); block: the same for all lanes
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int block)
-    {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, block * kBlockBytes, 0);
-        w = make_uint2(v.x, v.y);
-    }
     __device__ __forceinline__ v4i weights(int s) const
     {
         uint32_t a, b, c, d;
         decode_ternary(s ? w.y : w.x, a, b, c, d);
         return v4i{(int)a, (int)b, (int)c, (int)d};
-    }
-    static __device__ __forceinline__ v4i acts(uint4 lo, uint4 hi, int s)
-    {
-        return s ? transpose4(hi.x, hi.y, hi.z, hi.w) : transpose4(lo.x, lo.y, lo.z, lo.w);
     }
 };
 // Sign: lane group g holds word g of a block's 4, the weights 32 g .. 32 g + 31; bit j of its
@@ -172,10 +162,6 @@ struct Core<TB_FMT_SIGN1> {
     static constexpr int kStep = 16;
     static constexpr int kBlockBytes = 16;
     uint32_t w;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int block)
-    {
-        w = __builtin_amdgcn_raw_buffer_load_b32(r, off, block * kBlockBytes, 0);
-    }
     __device__ __forceinline__ v4i weights(int s) const
     {
         v4i o;
@@ -183,10 +169,6 @@ struct Core<TB_FMT_SIGN1> {
         for (int j = 0; j < 4; ++j)
             o[j] = (int)__builtin_amdgcn_perm(0u, 0x000001FFu, (w >> (4 * s + j)) & 0x01010101u);
         return o;
-    }
-    static __device__ __forceinline__ v4i acts(uint4 lo, uint4 hi, int s)
-    {
-        return s ? transpose4(lo.y, lo.w, hi.y, hi.w) : transpose4(lo.x, lo.z, hi.x, hi.z);
     }
 };
 
@@ -211,23 +193,34 @@ struct MoeArgs {
 //     weight row i. So a lane folds the row whose codes and scales it loaded itself. Pair t of
 //     16 is A row 4 (t % 4) + t / 4: element e of lane group g is pair g + 4 e, and a tile of up to
 //     4 pairs folds one element.
-//   * A wave owns two tiles of 16 weight rows (gate/up: the same rows of both) through all of k;
-//     nothing of a row crosses waves. The blocks of a step are taken in the order in which the
+//   * A wave owns tiles of 16 weight rows through all of k; nothing of a row crosses waves. The blocks of a step are taken in the order in which the
 //     step's tree adds them: 0, last, last - 1, last - 2, then the next four downwards. Such a phase
 //     of 4 blocks leaves one partial sum, the tree above it one register set per level.
-//   * Activations are staged in LDS as the operands read them: byte-transposed, 16 bytes per lane;
-//     slot row ^ 2 g keeps reads and writes free of bank conflicts.
+//   * Activations are staged in LDS as the operands read them: byte-transposed, 16 bytes per lane,
+//     in planes (block, instruction, lane group) of A rows.
 //   * Blocks past the end of k have dq = 0 and count +0.
 // ------------------------------------------------------------------------------------
-constexpr int kTilesPerWave = 2;
-
-// Block `b` (0 .. 3) of phase p: its index in k.
+// Stages piece `unit` (16 activations) of block u of A row `row`: lanes 8 x .. 8 x + 7 hold the pieces of
+// a block. A piece goes to the plane (block, instruction s, lane group g) whose code word it meets
+// (StepRow); planes are `pitch` rows of 16 bytes, and the odd pitch spreads the pieces over the banks.
 template <int FMT>
-__device__ __forceinline__ int phase_block(int p, int b)
+__device__ __forceinline__ void stage_piece(uint8_t *lds, int pitch, int u, int row, int unit, uint4 v)
 {
-    constexpr int kStep = Core<FMT>::kStep, kPhases = kStep / 4;
-    const int j = 4 * (p % kPhases) + b;
-    return p / kPhases * kStep + (j ? kStep - j : 0);
+    v4i o;
+    int s, g;
+    if constexpr (FMT == TB_FMT_TERNARY2) {
+        // word w: instruction w % 2, lane group 0, 2, 1, 3 for words 0, 2, 4, 6
+        s = unit & 1;
+        g = (unit & 2) | unit >> 2;
+        o = transpose4(v.x, v.y, v.z, v.w);
+    } else {
+        // a word meets two pieces: the even lane makes instruction 0's bytes, the odd lane 1's
+        s = unit & 1;
+        g = unit >> 1;
+        const uint32_t x = row_xor(s ? v.x : v.y, 1), y = row_xor(s ? v.z : v.w, 1);
+        o = s ? transpose4(x, y, v.y, v.w) : transpose4(v.x, v.z, x, y);
+    }
+    reinterpret_cast<v4i *>(lds)[(u * 8 + s * 4 + g) * pitch + row] = o;
 }
 
 // A row of a tile's pair t
@@ -240,27 +233,32 @@ __device__ __forceinline__ size_t act_row(const MoeArgs &a, int slot)
     return TWO ? (unsigned)min(max(a.order[slot], 0), a.pairs - 1) / (unsigned)a.topk : (unsigned)slot;
 }
 
-// The lane's rows of a wave's two tiles. Rows past n read the last one and are not stored.
-template <int FMT, bool TWO>
+// A lane's weight row: column `at` of the output, of matrix m. Rows past n read the last one and are
+// not stored.
+template <int FMT>
 struct WeightRows {
-    __amdgpu_buffer_rsrc_t codes[2], scales[2];
-    uint32_t coff[2], soff[2];   // byte offsets of the row's codes and scales
-    int col[2];
-    __device__ __forceinline__ WeightRows(const MoeArgs &a, int expert, int n0, int wave, int i, int nb)
+    __amdgpu_buffer_rsrc_t codes, scales;
+    uint32_t coff, soff;   // byte offsets of the row's codes and scales
+    int col;
+    uint32_t base;
+    __device__ __forceinline__ WeightRows(const MoeArgs &a, int m, int expert, int at, int nb)
     {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int m = TWO ? r : 0;
-            col[r] = n0 + 16 * (TWO ? wave : 2 * wave + r) + i;
-            const uint32_t row = min(col[r], a.n - 1);
-            const size_t first = (size_t)expert * a.n * nb, blocks = (size_t)a.n * nb;
-            codes[r] = buffer_rsrc(a.codes[m] + first * Core<FMT>::kBlockBytes, (uint32_t)(blocks * Core<FMT>::kBlockBytes));
-            coff[r] = row * (nb * Core<FMT>::kBlockBytes);
-            // the scales buffer starts, and ends, at whole words
-            const size_t odd = first & 1;
-            scales[r] = buffer_rsrc(a.scales[m] + (first - odd), (uint32_t)((blocks + odd + 1) / 2 * 4));
-            soff[r] = (row * nb + (uint32_t)odd) * 2;
-        }
+        col = at;
+        const uint32_t row = min(at, a.n - 1);
+        const size_t first = (size_t)expert * a.n * nb, blocks = (size_t)a.n * nb;
+        codes = buffer_rsrc((m ? a.codes[1] : a.codes[0]) + first * Core<FMT>::kBlockBytes, (uint32_t)(blocks * Core<FMT>::kBlockBytes));
+        coff = row * (nb * Core<FMT>::kBlockBytes);
+        // the scales buffer starts, and ends, at whole words
+        const size_t odd = first & 1;
+        scales = buffer_rsrc((m ? a.scales[1] : a.scales[0]) + (first - odd), (uint32_t)((blocks + odd + 1) / 2 * 4));
+        soff = (row * nb + (uint32_t)odd) * 2;
+        base = (uint32_t)odd * 2;
+    }
+    __device__ __forceinline__ void move(const MoeArgs &a, int at, int nb)
+    {
+        const uint32_t row = min(at, a.n - 1);
+        coff = row * (nb * Core<FMT>::kBlockBytes);
+        soff = row * nb * 2 + base;
     }
 };
 
@@ -278,25 +276,14 @@ __device__ __forceinline__ void add_phase(int q, float v, float &part0, float &p
         acc += part0 + (PHASES == 4 ? part1 + v : v);
 }
 
-// h of a gate/up lane, or the down outputs of its two rows, for pair `tok` of the tile.
+// The output row of pair `tok` of the tile (gate/up: h of its slot); null: there is none.
 template <bool TWO>
-__device__ __forceinline__ void store_pair(const MoeArgs &a, const Tile &tile, int tok, const int (&col)[2], float v0, float v1)
+__device__ __forceinline__ float *pair_out(const MoeArgs &a, const Tile &tile, int tok)
 {
     if (tok >= tile.rows)
-        return;
+        return nullptr;
     const int row = TWO ? tile.slot + tok : a.order[tile.slot + tok];
-    if ((unsigned)row >= (unsigned)a.pairs)
-        return;
-    float *o = a.out + (size_t)row * a.n;
-    if (TWO) {
-        if (col[0] < a.n)
-            o[col[0]] = silu_gate(v0, v1);
-    } else {
-        if (col[0] < a.n)
-            o[col[0]] = v0;
-        if (col[1] < a.n)
-            o[col[1]] = v1;
-    }
+    return (unsigned)row < (unsigned)a.pairs ? a.out + (size_t)row * a.n : nullptr;
 }
 
 // This workgroup's item of total * nblk: in expert order, dealt to the XCDs in contiguous ranges
@@ -316,262 +303,9 @@ __device__ __forceinline__ bool take_item(const MoeArgs &a, uint32_t b, int nblk
     return true;
 }
 
-// ------------------------------------------------------------------------------------
-// Many pairs per expert: 64 pairs, 8 waves, 256 weight rows; gate/up: 128 rows of each, whose h is
-// one rotation block, rotated and quantised from LDS at the end. A phase's activations are
-// staged, and the next phase's codes and scales loaded, while the last phase computes.
-// What bounds it: the fold's vector operations, 16 per lane for a 16x16 tile of one block (convert,
-// two products, a sum, 4 values each: 64 cycles) against 32 cycles of matrix instructions.
-// ------------------------------------------------------------------------------------
-template <int FMT, bool TWO>
-struct WideShape {
-    static constexpr int kWaves = 8, kThreads = 64 * kWaves;
-    static constexpr int kT = 64;                             // pairs of a tile
-    static constexpr int kCols = TWO ? 16 * kWaves : 32 * kWaves;
-    static constexpr int kPhases = Core<FMT>::kStep / 4;      // phases of a step
-    static constexpr int kItems = 4 * kT * 4 / kThreads;      // 32-byte staging items of a thread
-    static constexpr int kActBytes = 4 * kT * 128, kDqBytes = 4 * kT * 4;
-    static constexpr int kBufBytes = kActBytes + kDqBytes;
-    static constexpr int kHPitch = 132;                       // floats of a row of h in LDS
-    static constexpr int kLds = 2 * kBufBytes;
-    static_assert(kLds >= kT * kHPitch * 4, "h of the tile takes the staging buffers");
-};
-
-// NT: 16-pair groups in the tile.
-template <int FMT, bool TWO, int NT>
-__device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile, int n0, uint8_t *lds)
-{
-    using C = Core<FMT>;
-    using S = WideShape<FMT, TWO>;
-    constexpr int R = kTilesPerWave;
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 15, g = l >> 4;
-    const int nb = a.k / kBlock, np = (nb + C::kStep - 1) / C::kStep * S::kPhases;
-
-    const WeightRows<FMT, TWO> rows(a, tile.expert, n0, wave, i, nb);
-    C w[R][4];
-    uint16_t sc[R][4];
-    auto load_weights = [&](int h, int p) {   // blocks 2h, 2h + 1 of phase p
-#pragma unroll
-        for (int b = 2 * h; b < 2 * h + 2; ++b) {
-            const int at = min(phase_block<FMT>(p, b), nb - 1);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                w[r][b].load(rows.codes[r], rows.coff[r] + g * (C::kBlockBytes / 4), at);
-                sc[r][b] = __builtin_amdgcn_raw_buffer_load_b16(rows.scales[r], rows.soff[r], at * 2, 0);
-            }
-        }
-    };
-    load_weights(0, 0);
-    load_weights(1, 0);
-
-    // staging: a thread takes 32 activations (lane group sg of a block of a pair) at a time, a
-    // wave 16 pairs of one block
-    const int sg = tid & 3;
-    const int8_t *src[S::kItems];
-#pragma unroll
-    for (int it = 0; it < S::kItems; ++it) {
-        const int tok = (tid / 4 + it * (S::kThreads / 4)) % S::kT;
-        src[it] = a.q + act_row<TWO>(a, tile.slot + min(tok, tile.rows - 1)) * a.k + sg * 32;
-    }
-    const float *dsrc = a.dq + act_row<TWO>(a, tile.slot + min(l, tile.rows - 1)) * nb;
-    uint4 lo[S::kItems], hi[S::kItems];
-    float dv;
-    auto stage_load = [&](int p) {
-#pragma unroll
-        for (int it = 0; it < S::kItems; ++it) {
-            const int u = (16 * wave + it * (S::kThreads / 4)) / S::kT;
-            const uint4 *q = reinterpret_cast<const uint4 *>(src[it] + (size_t)min(phase_block<FMT>(p, u), nb - 1) * kBlock);
-            lo[it] = q[0];
-            hi[it] = q[1];
-        }
-        const int blk = wave < 4 ? phase_block<FMT>(p, wave) : nb;
-        dv = blk < nb ? dsrc[blk] : 0.0f;
-    };
-    auto stage_store = [&](int p) {
-        uint8_t *buf = lds + (p & 1) * S::kBufBytes;
-#pragma unroll
-        for (int it = 0; it < S::kItems; ++it) {
-            const int u = (16 * wave + it * (S::kThreads / 4)) / S::kT, tok = (tid / 4 + it * (S::kThreads / 4)) % S::kT;
-            v4i *q = reinterpret_cast<v4i *>(buf) + (u * 8 + sg) * S::kT + (pair_row(tok) ^ (2 * sg));
-            q[0] = C::acts(lo[it], hi[it], 0);
-            q[4 * S::kT] = C::acts(lo[it], hi[it], 1);
-        }
-        if (wave < 4)
-            reinterpret_cast<float *>(buf + S::kActBytes)[wave * S::kT + pair_row(l)] = dv;
-    };
-
-    float acc[R][NT][4], part0[R][NT][4], part1[R][NT][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[r][t][e] = 0.0f;
-    stage_load(0);
-    stage_store(0);
-    __syncthreads();
-
-    for (int p0 = 0; p0 < np; p0 += S::kPhases) {
-#pragma unroll
-        for (int j = 0; j < S::kPhases; ++j) {
-            const int p = p0 + j;
-            if (p + 1 < np)
-                stage_load(p + 1);
-            const uint8_t *buf = lds + (p & 1) * S::kBufBytes;
-            const v4i *act = reinterpret_cast<const v4i *>(buf) + g * S::kT;
-            const float *d = reinterpret_cast<const float *>(buf + S::kActBytes) + 4 * g;
-            float sum[R][NT][4];
-            // operands of group x = (half of the phase, 16 pairs): the next group's are read
-            // before this one is multiplied and folded (sign's tree has no registers left for it)
-            v4i av[2][2][2];
-            float dq[2][2][4];
-            auto operands = [&](int x) {
-                const int h = x / NT, t = x % NT;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int blk = 2 * h + b, slot = 16 * t + (i ^ (2 * g));
-                    av[x & 1][b][0] = act[(blk * 2) * 4 * S::kT + slot];
-                    av[x & 1][b][1] = act[(blk * 2 + 1) * 4 * S::kT + slot];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dq[x & 1][b][e] = d[blk * S::kT + 16 * t + e];
-                }
-            };
-            constexpr bool kEarly = FMT == TB_FMT_TERNARY2;
-            if (kEarly)
-                operands(0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {   // blocks 2h, 2h + 1
-                v4i wt[R][2][2];
-                float s[R][2];
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        wt[r][b][0] = w[r][2 * h + b].weights(0);
-                        wt[r][b][1] = w[r][2 * h + b].weights(1);
-                        s[r][b] = half_bits_to_float(sc[r][2 * h + b]);
-                    }
-                if (p + 1 < np)
-                    load_weights(h, p + 1);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int x = h * NT + t;
-                    if (!kEarly)
-                        operands(x);
-                    else if (x + 1 < 2 * NT)
-                        operands(x + 1);
-                    float term[R][2][4];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            v4i z = {0, 0, 0, 0};
-                            z = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[x & 1][b][0], wt[r][b][0], z, 0, 0, 0);
-                            z = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[x & 1][b][1], wt[r][b][1], z, 0, 0, 0);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                term[r][b][e] = (s[r][b] * dq[x & 1][b][e]) * (float)z[e];
-                        }
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float v = term[r][0][e] + term[r][1][e];
-                            sum[r][t][e] = h ? sum[r][t][e] + v : v;
-                            // the group's operations are pure: held here, or they sink below
-                            // the next groups' operand reads, which then all stay in registers
-                            asm volatile("" : "+v"(sum[r][t][e]));
-                        }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        add_phase<S::kPhases>(j, sum[r][t][e], part0[r][t][e], part1[r][t][e], acc[r][t][e]);
-            if (p + 1 < np)
-                stage_store(p + 1);
-            __syncthreads();
-        }
-    }
-
-    if constexpr (TWO) {   // h of the tile through LDS (the staging buffers are free), then its rotation
-        float *hs = reinterpret_cast<float *>(lds);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                hs[(16 * t + g + 4 * e) * S::kHPitch + 16 * wave + i] = silu_gate(acc[0][t][e], acc[1][t][e]);
-        __syncthreads();
-        const int lane16 = tid & 15;
-        for (int tok = tid >> 4; tok < tile.rows; tok += S::kThreads / 16) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = hs[tok * S::kHPitch + lane16 * 8 + e];
-            uint32_t packed[2];
-            float dq;
-            int qsum;
-            rotquant_regs(v, lane16, a.unit, packed, dq, qsum);
-            const size_t slot = tile.slot + tok;
-            *reinterpret_cast<uint2 *>(a.qh + slot * a.n + n0 + lane16 * 8) = make_uint2(packed[0], packed[1]);
-            if (lane16 == 0)
-                a.dqh[slot * (a.n / kBlock) + n0 / kBlock] = dq;
-        }
-    } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                store_pair<TWO>(a, tile, 16 * t + g + 4 * e, rows.col, acc[0][t][e], acc[1][t][e]);
-    }
-}
-
-template <int FMT, bool TWO>
-__global__ __launch_bounds__(512) void moe_wide_kernel(MoeArgs a, uint32_t first)
-{
-    using S = WideShape<FMT, TWO>;
-    __shared__ __align__(16) uint8_t lds[S::kLds];
-    Tile tile;
-    int block;
-    if (!take_item<S::kT>(a, first + blockIdx.x, (a.n + S::kCols - 1) / S::kCols, tile, block))
-        return;
-    const int n0 = block * S::kCols;
-    if (tile.rows <= 16)
-        wide_product<FMT, TWO, 1>(a, tile, n0, lds);
-    else if (tile.rows <= 32)
-        wide_product<FMT, TWO, 2>(a, tile, n0, lds);
-    else if (tile.rows <= 48)
-        wide_product<FMT, TWO, 3>(a, tile, n0, lds);
-    else
-        wide_product<FMT, TWO, 4>(a, tile, n0, lds);
-}
-
-// ------------------------------------------------------------------------------------
-// Few pairs per expert: 16 pairs, 4 waves of 32 weight rows, so that the experts' rows spread over
-// the chip; the weights' way from memory bounds it. A wave loads a whole step of its rows at once,
-// 256 bytes per row in four loads of 64 (smaller pieces fetch each 128-byte line several times),
-// one step ahead; lane swaps (v_permlane32_swap, sign also v_permlane16_swap) then deal the 16
-// bytes that lane group g holds, part of one block, out to all groups. Up to 32 blocks of the
-// activations there are are staged at a time.
-// ------------------------------------------------------------------------------------
-template <int FMT, bool TWO>
-struct NarrowShape {
-    static constexpr int kWaves = 4, kThreads = 64 * kWaves;
-    static constexpr int kT = 16;
-    static constexpr int kCols = TWO ? 16 * kWaves : 32 * kWaves;
-    static constexpr int kPhases = Core<FMT>::kStep / 4;
-    static constexpr int kBlocks = 32;                        // staged at a time
-    static constexpr int kActBytes = kBlocks * kT * 128, kDqBytes = kBlocks * kT * 4;
-    static constexpr int kLds = kActBytes + kDqBytes;
-};
-
-// A step of the lane's row: codes[x] is bytes 64 x + 16 g .. + 15 of the step's 256, scales the step's.
+// A step of the lane's row, loaded as a whole: 256 bytes of codes in four loads of 64 per row (loads of
+// a block, 8 bytes a lane, kept the address unit busy for 40% of the wide kernel's time, and
+// fetched each 128-byte line several times). codes[x] is bytes 64 x + 16 g .. + 15 of the step's 256, scales the step's.
 template <int FMT>
 struct StepRow {
     static constexpr int kScaleWords = Core<FMT>::kStep / 2;
@@ -599,7 +333,7 @@ struct StepRow {
         }
         scales[kScaleWords] = buffer_load_u32(s, so + kScaleWords * 4);
     }
-    // After the loads: each block's codes in all lane groups, scales from bit 0 of scales[0] on.
+    // After the loads, by lane swaps: each block's codes, 16 bytes of which one lane group loaded, in all groups, scales from bit 0 of scales[0] on.
     // odd: the row's first scale is the upper half of its word
     __device__ __forceinline__ void deal(bool odd)
     {
@@ -642,42 +376,262 @@ struct StepRow {
     }
 };
 
+// ------------------------------------------------------------------------------------
+// Many pairs per expert: 48 pairs, 16 waves of 16 weight rows; gate/up: 128 rows of each, whose h is
+// one rotation block, rotated and quantised from LDS at the end. Up to 16 blocks of the pairs'
+// activations stay in LDS; a workgroup takes several row groups with them, and while they fit
+// (k <= 2048) its waves run through them without meeting. The next step's codes are loaded while the
+// last half phase of a step is multiplied.
+// What bounds it: the fold's vector operations, 16 per lane for a 16x16 tile of one block (a
+// difference, two products, a sum, 4 values each), the decode and 32 cycles of matrix instructions.
+// 16 waves per CU, because a wave alone issues a vector operation every 5 to 6 cycles and four of a
+// SIMD together one every 2.3.
+// ------------------------------------------------------------------------------------
+template <int FMT, bool TWO>
+struct WideShape {
+    static constexpr int kWaves = 16, kThreads = 64 * kWaves;
+    static constexpr int kT = 48;                             // pairs of a tile
+    static constexpr int kPairsPerWave = kT / kWaves;         // that a wave stages
+    static constexpr int kCols = TWO ? 8 * kWaves : 16 * kWaves;
+    static constexpr int kPhases = Core<FMT>::kStep / 4;      // phases of a step
+    static constexpr int kBlocks = 16;                        // staged at a time
+    static constexpr int kPitch = kT + 1;                     // A rows of a plane: odd, so that a pair's 64 pieces of 16 bytes spread over the banks
+    static constexpr int kActBytes = kBlocks * 8 * kPitch * 16, kDqBytes = kBlocks * kT * 4;
+    static constexpr int kHPitch = 132;                       // floats of a row of g or u in LDS
+    static constexpr int kLds = kActBytes + kDqBytes + (TWO ? 2 * kT * kHPitch * 4 : 0);
+    static_assert(kLds <= 160 * 1024 && kBlocks * kT <= kThreads, "");
+};
+
+// The block sum's fp32 value comes from the integer accumulator by one subtraction: it starts at
+// the bits of 1.5 * 2^23, so that its bits are those of 1.5 * 2^23 + sum (|sum| <= 128 * 127 < 2^22).
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.0f;
+
+// Row groups [j0, j1) of the tile's expert. NT: 16-pair groups in the tile.
+template <int FMT, bool TWO, int NT>
+__device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile, int j0, int j1, uint8_t *lds)
+{
+    using C = Core<FMT>;
+    using S = WideShape<FMT, TWO>;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 15, g = l >> 4;
+    const int nb = a.k / kBlock, steps = (nb + C::kStep - 1) / C::kStep;
+    const int col0 = 16 * (TWO ? wave & 7 : wave) + i, mat = TWO ? wave >> 3 : 0;
+    float *dq_s = reinterpret_cast<float *>(lds + S::kActBytes);
+
+    StepRow<FMT> w;
+    WeightRows<FMT> rows(a, mat, tile.expert, j0 * S::kCols + col0, nb);
+    auto load_weights = [&](int step) { w.load(rows.codes, rows.scales, rows.coff + g * 16, rows.soff & ~3u, nb, step); };
+    load_weights(0);
+
+    // blocks [c0, c0 + kBlocks): a wave takes kPairsPerWave pairs, 1 KB of each at a time
+    auto stage = [&](int c0) {
+        uint4 v[S::kPairsPerWave][2];
+#pragma unroll
+        for (int t = 0; t < S::kPairsPerWave; ++t) {
+            const int tok = min(wave * S::kPairsPerWave + t, tile.rows - 1);
+            const int8_t *src = a.q + act_row<TWO>(a, tile.slot + tok) * a.k;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)   // pieces past the end of k read its last block
+                v[t][h] = *reinterpret_cast<const uint4 *>(src + min((c0 + 8 * h) * kBlock + l * 16, (nb - 1) * kBlock + (l & 7) * 16));
+        }
+        float d = 0.0f;
+        if (tid < S::kBlocks * S::kT && c0 + tid % S::kBlocks < nb)
+            d = a.dq[act_row<TWO>(a, tile.slot + min(tid / S::kBlocks, tile.rows - 1)) * nb + c0 + tid % S::kBlocks];
+#pragma unroll
+        for (int t = 0; t < S::kPairsPerWave; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                stage_piece<FMT>(lds, S::kPitch, 8 * h + (l >> 3), pair_row(wave * S::kPairsPerWave + t), l & 7, v[t][h]);
+        if (tid < S::kBlocks * S::kT)
+            dq_s[tid % S::kBlocks * S::kT + pair_row(tid / S::kBlocks)] = d;
+    };
+    stage(0);
+    __syncthreads();
+
+    for (int jn = j0; jn < j1; ++jn) {
+        const int n0 = jn * S::kCols;
+        float acc[NT][4], part0[NT][4], part1[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[t][e] = 0.0f;
+        for (int step = 0; step < steps; ++step) {
+            const int u0 = step * C::kStep % S::kBlocks;
+            if (nb > S::kBlocks && u0 == 0 && (step || jn > j0)) {
+                __syncthreads();
+                stage(step * C::kStep);
+                __syncthreads();
+            }
+            const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kPitch + i;
+            const float *d = dq_s + u0 * S::kT + 4 * g;
+            w.deal(rows.soff & 2);
+#pragma unroll
+            for (int j = 0; j < S::kPhases; ++j) {
+                float sum[NT][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {   // two blocks of the phase
+                    int blk[2];
+                    v4i wt[2][2];
+                    float s[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int x = 4 * j + 2 * h + b;
+                        blk[b] = x ? C::kStep - x : 0;   // block of the step
+                        const C core = w.block(blk[b]);
+                        wt[b][0] = core.weights(0);
+                        wt[b][1] = core.weights(1);
+                        s[b] = w.scale(blk[b]);
+                        // decoded here, not below the loads that take the codes' registers
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            asm volatile("" : "+v"(wt[b][0][e]), "+v"(wt[b][1][e]));
+                        asm volatile("" : "+v"(s[b]));
+                    }
+                    if (j == S::kPhases - 1 && h == 1) {   // the step's codes are used up
+                        if (step + 1 < steps) {
+                            load_weights(step + 1);
+                        } else if (jn + 1 < j1) {
+                            rows.move(a, col0 + n0 + S::kCols, nb);
+                            load_weights(0);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float term[2][4];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const v4i a0 = act[blk[b] * 8 * S::kPitch + 16 * t], a1 = act[(blk[b] * 8 + 4) * S::kPitch + 16 * t];
+                            v4i z = {kMagicBits, kMagicBits, kMagicBits, kMagicBits};
+                            z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, wt[b][0], z, 0, 0, 0);
+                            z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, wt[b][1], z, 0, 0, 0);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                term[b][e] = (s[b] * d[blk[b] * S::kT + 16 * t + e]) * (__int_as_float(z[e]) - kMagic);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float v = term[0][e] + term[1][e];
+                            sum[t][e] = h ? sum[t][e] + v : v;
+                            // the group's operations are pure: held here, or they sink below the
+                            // next groups' operand reads, which then all stay in registers
+                            asm volatile("" : "+v"(sum[t][e]));
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        add_phase<S::kPhases>(j, sum[t][e], part0[t][e], part1[t][e], acc[t][e]);
+            }
+        }
+
+        if constexpr (TWO) {   // g and u through LDS, then h and its rotation
+            float *hs = reinterpret_cast<float *>(lds + S::kActBytes + S::kDqBytes);
+            __syncthreads();   // the last row group's h has been read
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    hs[(mat * S::kT + 16 * t + g + 4 * e) * S::kHPitch + col0] = acc[t][e];
+            __syncthreads();
+            const int lane16 = tid & 15, pair = tid >> 4;
+            static_assert(S::kThreads / 16 >= S::kT, "16 lanes for each pair");
+            if (pair < tile.rows) {
+                const float *gp = hs + pair * S::kHPitch + lane16 * 8, *up = gp + S::kT * S::kHPitch;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = silu_gate(gp[e], up[e]);
+                uint32_t packed[2];
+                float dq;
+                int qsum;
+                rotquant_regs(v, lane16, a.unit, packed, dq, qsum);
+                const size_t slot = tile.slot + pair;
+                *reinterpret_cast<uint2 *>(a.qh + slot * a.n + n0 + lane16 * 8) = make_uint2(packed[0], packed[1]);
+                if (lane16 == 0)
+                    a.dqh[slot * (a.n / kBlock) + n0 / kBlock] = dq;
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (float *o = pair_out<TWO>(a, tile, 16 * t + g + 4 * e))
+                        if (n0 + col0 < a.n)
+                            o[n0 + col0] = acc[t][e];
+        }
+    }
+}
+
+// groups: workgroups of a tile; each takes its share of the row groups.
+template <int FMT, bool TWO>
+__global__ __launch_bounds__(1024) void moe_wide_kernel(MoeArgs a, uint32_t first, int groups)
+{
+    using S = WideShape<FMT, TWO>;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
+    Tile tile;
+    int group;
+    if (!take_item<S::kT>(a, first + blockIdx.x, groups, tile, group))
+        return;
+    const int nblk = (a.n + S::kCols - 1) / S::kCols, j0 = part_lo(nblk, groups, group), j1 = part_lo(nblk, groups, group + 1);
+    if (tile.rows <= 16)
+        wide_product<FMT, TWO, 1>(a, tile, j0, j1, lds);
+    else if (tile.rows <= 32)
+        wide_product<FMT, TWO, 2>(a, tile, j0, j1, lds);
+    else
+        wide_product<FMT, TWO, 3>(a, tile, j0, j1, lds);
+}
+
+// ------------------------------------------------------------------------------------
+// Few pairs per expert: 16 pairs, 4 waves of 32 weight rows, so that the experts' rows spread over
+// the chip; the weights' way from memory bounds it. Steps are loaded one ahead, and up to 32 blocks of
+// the activations there are are staged at a time.
+// ------------------------------------------------------------------------------------
+template <int FMT, bool TWO>
+struct NarrowShape {
+    static constexpr int kWaves = 4, kThreads = 64 * kWaves;
+    static constexpr int kT = 16;
+    static constexpr int kCols = TWO ? 16 * kWaves : 32 * kWaves;
+    static constexpr int kPhases = Core<FMT>::kStep / 4;
+    static constexpr int kBlocks = 32;                        // staged at a time
+    static constexpr int kPitch = kT + 1;
+    static constexpr int kActBytes = kBlocks * 8 * kPitch * 16, kDqBytes = kBlocks * kT * 4;
+    static constexpr int kLds = kActBytes + kDqBytes;
+};
+
 // NE: elements that hold pairs.
 template <int FMT, bool TWO, int NE>
 __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &tile, int n0, uint8_t *lds)
 {
     using C = Core<FMT>;
     using S = NarrowShape<FMT, TWO>;
-    constexpr int R = kTilesPerWave;
+    constexpr int R = 2;   // row tiles of a wave (gate/up: the same rows of both)
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 15, g = l >> 4;
     const int nb = a.k / kBlock, steps = (nb + C::kStep - 1) / C::kStep;
 
-    const WeightRows<FMT, TWO> rows(a, tile.expert, n0, wave, i, nb);
+    WeightRows<FMT> rows[R] = {{a, 0, tile.expert, n0 + 16 * (TWO ? wave : 2 * wave) + i, nb},
+                                     {a, TWO ? 1 : 0, tile.expert, n0 + 16 * (TWO ? wave : 2 * wave + 1) + i, nb}};
     StepRow<FMT> w[2][R];
     auto load_weights = [&](int j, int step) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            w[j][r].load(rows.codes[r], rows.scales[r], rows.coff[r] + g * 16, rows.soff[r] & ~3u, nb, step);
+            w[j][r].load(rows[r].codes, rows[r].scales, rows[r].coff + g * 16, rows[r].soff & ~3u, nb, step);
     };
     load_weights(0, 0);
 
-    // staging: 128 threads for the 4 lane groups (32 activations each) of 32 blocks of a pair
-    const int sg = tid & 3, u = (tid & 127) >> 2;
-    // the lane group that reads the words of staging group sg
-    const int to = FMT == TB_FMT_TERNARY2 ? (sg & 1) << 1 | sg >> 1 : sg;
+    // staging: 8 blocks of a pair by a wave, 32 by the workgroup
     auto stage = [&](int c0) {
-        const int blk = c0 + u, at = min(blk, nb - 1);
+        const int u = tid >> 3, at = min(c0 + u, nb - 1);
 #pragma unroll 4
-        for (int tok = wave >> 1; tok < tile.rows; tok += S::kThreads / 128) {
+        for (int tok = 0; tok < tile.rows; ++tok) {
             const size_t row = act_row<TWO>(a, tile.slot + tok);
-            const uint4 *p = reinterpret_cast<const uint4 *>(a.q + row * a.k + (size_t)at * kBlock + sg * 32);
-            const uint4 lo = p[0], hi = p[1];
-            const float dq = blk < nb ? a.dq[row * nb + at] : 0.0f;
-            v4i *o = reinterpret_cast<v4i *>(lds) + (u * 8 + to) * S::kT + (pair_row(tok) ^ (2 * to));
-            o[0] = C::acts(lo, hi, 0);
-            o[4 * S::kT] = C::acts(lo, hi, 1);
-            if (sg == 0)
-                reinterpret_cast<float *>(lds + S::kActBytes)[u * S::kT + pair_row(tok)] = dq;
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.q + row * a.k + at * kBlock + (tid & 7) * 16);
+            stage_piece<FMT>(lds, S::kPitch, u, pair_row(tok), tid & 7, v);
+            if (tid < S::kBlocks)
+                reinterpret_cast<float *>(lds + S::kActBytes)[tid * S::kT + pair_row(tok)] = c0 + tid < nb ? a.dq[row * nb + c0 + tid] : 0.0f;
         }
     };
     if (steps > 1)
@@ -704,9 +658,9 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    w[j][r].deal(rows.soff[r] & 2);
+                    w[j][r].deal(rows[r].soff & 2);
                 const int u0 = step % kPer * C::kStep;
-                const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kT + (i ^ (2 * g));
+                const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kPitch + i;
                 const float *d = reinterpret_cast<const float *>(lds + S::kActBytes) + u0 * S::kT + 4 * g;
                 float part0[R][NE], part1[R][NE];
 #pragma unroll
@@ -718,7 +672,7 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int x = 4 * q + 2 * h + b, blk = x ? C::kStep - x : 0;
-                            const v4i a0 = act[blk * 8 * S::kT], a1 = act[(blk * 8 + 4) * S::kT];
+                            const v4i a0 = act[blk * 8 * S::kPitch], a1 = act[(blk * 8 + 4) * S::kPitch];
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
                                 const C core = w[j][r].block(blk);
@@ -755,7 +709,12 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
     }
 #pragma unroll
     for (int e = 0; e < NE; ++e)
-        store_pair<TWO>(a, tile, g + 4 * e, rows.col, acc[0][e], acc[1][e]);
+        if (float *o = pair_out<TWO>(a, tile, g + 4 * e)) {
+            if (rows[0].col < a.n)
+                o[rows[0].col] = TWO ? silu_gate(acc[0][e], acc[1][e]) : acc[0][e];
+            if (!TWO && rows[1].col < a.n)
+                o[rows[1].col] = acc[1][e];
+        }
 }
 
 template <int FMT, bool TWO>
@@ -840,22 +799,22 @@ int check_pairs(int tokens, int topk)
     return (int64_t)tokens * topk > 0x7fffffc0 ? TB_EUNSUPPORTED : TB_OK;
 }
 
-template <class S>
-int launch_tiles(const MoeArgs &a, void (*kernel)(MoeArgs, uint32_t), hipStream_t stream)
+// Launches items of tiles * parts in grids of up to kMaxGrid workgroups.
+template <class F>
+int launch_items(int64_t tiles, int parts, F &&launch)
 {
-    // every expert's last tile may be partly filled, and no tile is empty
-    const int64_t tiles = std::min<int64_t>(a.pairs, (int64_t)a.pairs / S::kT + a.experts);
-    const int64_t total = tiles * ((a.n + S::kCols - 1) / S::kCols);
+    const int64_t total = tiles * parts;
     if (total > 0x7fffffff)
         return TB_EUNSUPPORTED;
     for (int64_t first = 0; first < total; first += kMaxGrid) {
-        const int64_t grid = std::min<int64_t>((total - first + kXcds - 1) / kXcds * kXcds, kMaxGrid);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::kThreads), 0, stream, a, (uint32_t)first);
+        launch(dim3((unsigned)std::min<int64_t>((total - first + kXcds - 1) / kXcds * kXcds, kMaxGrid)), (uint32_t)first);
         if (hipGetLastError() != hipSuccess)
             return TB_EHIP;
     }
     return TB_OK;
 }
+// Tiles of `rows` pairs at most: every expert's last may be partly filled, and none is empty.
+int64_t most_tiles(const MoeArgs &a, int rows) { return std::min<int64_t>(a.pairs, (int64_t)a.pairs / rows + a.experts); }
 
 // Wide tiles from an average of 16 pairs per expert on.
 bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)experts * 16; }
@@ -863,8 +822,21 @@ bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)expe
 template <int FMT, bool TWO>
 int launch_product_as(const MoeArgs &a, hipStream_t stream)
 {
-    return wide_tiles(a.pairs, a.experts) ? launch_tiles<WideShape<FMT, TWO>>(a, moe_wide_kernel<FMT, TWO>, stream)
-                                          : launch_tiles<NarrowShape<FMT, TWO>>(a, moe_narrow_kernel<FMT, TWO>, stream);
+    if (!wide_tiles(a.pairs, a.experts)) {
+        using S = NarrowShape<FMT, TWO>;
+        return launch_items(most_tiles(a, S::kT), (a.n + S::kCols - 1) / S::kCols, [&](dim3 grid, uint32_t first) {
+            hipLaunchKernelGGL((moe_narrow_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first);
+        });
+    }
+    using S = WideShape<FMT, TWO>;
+    // a tile's row groups go to as few workgroups as leave four for each CU, so that little is
+    // staged twice and the last workgroups end together
+    const int64_t tiles = most_tiles(a, S::kT);
+    const int nblk = (a.n + S::kCols - 1) / S::kCols;
+    const int groups = (int)std::min<int64_t>(nblk, (1024 + tiles - 1) / tiles);
+    return launch_items(tiles, groups, [&](dim3 grid, uint32_t first) {
+        hipLaunchKernelGGL((moe_wide_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first, groups);
+    });
 }
 template <bool TWO>
 int launch_product(const MoeArgs &a, int fmt, hipStream_t stream)
