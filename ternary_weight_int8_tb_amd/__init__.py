@@ -359,17 +359,22 @@ def _bad(fn: str, why: str):
     raise TbError(fn, TB_EINVAL, why)
 
 
+_DTYPES: dict = {}
+
+
 def _dtype(fn: str, t) -> int:
-    import torch
-    code = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.float16: TB_F16}.get(t.dtype)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.float16: TB_F16})
+    code = _DTYPES.get(t.dtype)
     if code is None:
         _bad(fn, f"{t.dtype} rows: float32, bfloat16 or float16 are wanted")
     return code
 
 
-def _check(fn: str, device, **tensors) -> None:
-    """Each of tensors is (tensor, dtype, shape): contiguous, on `device`."""
-    for name, (t, dtype, shape) in tensors.items():
+def _check(fn: str, device, *arrays) -> None:
+    """Each of arrays is (name, tensor, dtype, shape): contiguous, on `device`."""
+    for name, t, dtype, shape in arrays:
         if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
             _bad(fn, f"{name} has to be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
@@ -403,13 +408,13 @@ def tb_add_rmsnorm_quant_i8(x, res, gamma, eps: float, res_out, y, q, dq, stream
     m, k = _matrix_rows(fn, "x", x)
     dev, dt = x.device, x.dtype
     code = _dtype(fn, x)
-    _check(fn, dev, gamma=(gamma, torch.float32, (k,)), q=(q, torch.int8, (m, k)), dq=(dq, torch.float32, (m, k // BLOCK)))
+    _check(fn, dev, ("gamma", gamma, torch.float32, (k,)), ("q", q, torch.int8, (m, k)), ("dq", dq, torch.float32, (m, k // BLOCK)))
     if res is not None:
-        _check(fn, dev, res=(res, dt, (m, k)))
+        _check(fn, dev, ("res", res, dt, (m, k)))
     if res_out is not None:
-        _check(fn, dev, res_out=(res_out, dt, (m, k)))
+        _check(fn, dev, ("res_out", res_out, dt, (m, k)))
     if y is not None:
-        _check(fn, dev, y=(y, dt, (m, k)))
+        _check(fn, dev, ("y", y, dt, (m, k)))
     _launch(fn, dev, stream, x.data_ptr(), _ptr(res), gamma.data_ptr(), code, m, k, eps, _ptr(res_out), _ptr(y),
             q.data_ptr(), dq.data_ptr())
 
@@ -420,7 +425,7 @@ class Mxfp4:
     def __init__(self, codes, scales):
         import torch
         n, half = _matrix_rows("Mxfp4", "codes", codes)
-        _check("Mxfp4", codes.device, codes=(codes, torch.uint8, (n, half)), scales=(scales, torch.uint8, (n, half // 16)))
+        _check("Mxfp4", codes.device, ("codes", codes, torch.uint8, (n, half)), ("scales", scales, torch.uint8, (n, half // 16)))
         self.codes, self.scales, self.n, self.k, self.device = codes, scales, int(n), 2 * int(half), codes.device
         self.c = CMxfp4(codes.data_ptr(), scales.data_ptr(), self.n, self.k)
 
@@ -441,7 +446,7 @@ def tb_mxfp4_quant(x, codes, scales, rotate: bool = False, stream=None) -> None:
     fn = "tb_mxfp4_quant"
     m, k = _matrix_rows(fn, "x", x)
     code = _dtype(fn, x)
-    _check(fn, x.device, codes=(codes, torch.uint8, (m, k // 2)), scales=(scales, torch.uint8, (m, k // 32)))
+    _check(fn, x.device, ("codes", codes, torch.uint8, (m, k // 2)), ("scales", scales, torch.uint8, (m, k // 32)))
     _launch(fn, x.device, stream, x.data_ptr(), code, m, k, int(bool(rotate)), codes.data_ptr(), scales.data_ptr())
 
 
@@ -451,7 +456,7 @@ def tb_mxfp4_dequant(codes, scales, y, stream=None) -> None:
     fn = "tb_mxfp4_dequant"
     m, k = _matrix_rows(fn, "y", y)
     code = _dtype(fn, y)
-    _check(fn, y.device, codes=(codes, torch.uint8, (m, k // 2)), scales=(scales, torch.uint8, (m, k // 32)))
+    _check(fn, y.device, ("codes", codes, torch.uint8, (m, k // 2)), ("scales", scales, torch.uint8, (m, k // 32)))
     _launch(fn, y.device, stream, codes.data_ptr(), scales.data_ptr(), m, k, y.data_ptr(), code)
 
 
@@ -470,9 +475,9 @@ def tb_mxfp4_gemm(w: Mxfp4, codes, scales, y, ws=None, stream=None) -> None:
     code, dev = _dtype(fn, y), y.device
     if n != w.n or w.device != dev:
         _bad(fn, f"y has to have {w.n} columns, on {w.device}")
-    _check(fn, dev, codes=(codes, torch.uint8, (m, w.k // 2)), scales=(scales, torch.uint8, (m, w.k // 32)))
+    _check(fn, dev, ("codes", codes, torch.uint8, (m, w.k // 2)), ("scales", scales, torch.uint8, (m, w.k // 32)))
     if ws is not None:
-        _check(fn, dev, ws=(ws, torch.uint8, (ws.numel(),)))
+        _check(fn, dev, ("ws", ws, torch.uint8, (ws.numel(),)))
     _launch(fn, dev, stream, ctypes.byref(w.c), codes.data_ptr(), scales.data_ptr(), m, y.data_ptr(), code, _ptr(ws),
             0 if ws is None else ws.numel())
 
@@ -489,8 +494,8 @@ class Experts:
         if fmt not in (TB_FMT_TERNARY2, TB_FMT_SIGN1):
             _bad(fn, f"format {fmt}")
         e, n, nb = scales.shape
-        _check(fn, scales.device, codes=(codes, torch.uint8, (e, n, nb, 32 if fmt == TB_FMT_TERNARY2 else 16)),
-               scales=(scales, scales.dtype, (e, n, nb)))
+        _check(fn, scales.device, ("codes", codes, torch.uint8, (e, n, nb, 32 if fmt == TB_FMT_TERNARY2 else 16)),
+               ("scales", scales, scales.dtype, (e, n, nb)))
         self.codes, self.scales, self.device = codes, scales, scales.device
         self.experts, self.n, self.k, self.fmt = int(e), int(n), int(nb) * BLOCK, int(fmt)
         self.c = CExperts(codes.data_ptr(), scales.data_ptr(), self.experts, self.n, self.k, self.fmt)
@@ -513,8 +518,8 @@ def tb_moe_plan(ids, experts: int, offsets, order, stream=None) -> None:
     import torch
     fn = "tb_moe_plan"
     t, topk = _matrix_rows(fn, "ids", ids)
-    _check(fn, ids.device, ids=(ids, torch.int32, (t, topk)), offsets=(offsets, torch.int32, (experts + 1,)),
-           order=(order, torch.int32, (t * topk,)))
+    _check(fn, ids.device, ("ids", ids, torch.int32, (t, topk)), ("offsets", offsets, torch.int32, (experts + 1,)),
+           ("order", order, torch.int32, (t * topk,)))
     _launch(fn, ids.device, stream, ids.data_ptr(), t, topk, experts, offsets.data_ptr(), order.data_ptr())
 
 
@@ -530,8 +535,8 @@ def tb_moe_gateup_silu(wg: Experts, wu: Experts, q, dq, topk: int, offsets, orde
     if k != wg.k or wg.device != dev or wu.device != dev:
         _bad(fn, f"q has to have {wg.k} columns, on {wg.device}")
     i32, f32 = torch.int32, torch.float32
-    _check(fn, dev, q=(q, torch.int8, (t, k)), dq=(dq, f32, (t, k // BLOCK)), offsets=(offsets, i32, (wg.experts + 1,)),
-           order=(order, i32, (p,)), h=(h, f32, (p, n)), qh=(qh, torch.int8, (p, n)), dqh=(dqh, f32, (p, n // BLOCK)))
+    _check(fn, dev, ("q", q, torch.int8, (t, k)), ("dq", dq, f32, (t, k // BLOCK)), ("offsets", offsets, i32, (wg.experts + 1,)),
+           ("order", order, i32, (p,)), ("h", h, f32, (p, n)), ("qh", qh, torch.int8, (p, n)), ("dqh", dqh, f32, (p, n // BLOCK)))
     _launch(fn, dev, stream, ctypes.byref(wg.c), ctypes.byref(wu.c), q.data_ptr(), dq.data_ptr(), t, topk,
             offsets.data_ptr(), order.data_ptr(), h.data_ptr(), qh.data_ptr(), dqh.data_ptr())
 
@@ -545,8 +550,8 @@ def tb_moe_down(wd: Experts, qh, dqh, offsets, order, y, stream=None) -> None:
     if k != wd.k or wd.device != dev:
         _bad(fn, f"qh has to have {wd.k} columns, on {wd.device}")
     i32, f32 = torch.int32, torch.float32
-    _check(fn, dev, qh=(qh, torch.int8, (p, k)), dqh=(dqh, f32, (p, k // BLOCK)), offsets=(offsets, i32, (wd.experts + 1,)),
-           order=(order, i32, (p,)), y=(y, f32, (p, wd.n)))
+    _check(fn, dev, ("qh", qh, torch.int8, (p, k)), ("dqh", dqh, f32, (p, k // BLOCK)), ("offsets", offsets, i32, (wd.experts + 1,)),
+           ("order", order, i32, (p,)), ("y", y, f32, (p, wd.n)))
     _launch(fn, dev, stream, ctypes.byref(wd.c), qh.data_ptr(), dqh.data_ptr(), p, offsets.data_ptr(), order.data_ptr(),
             y.data_ptr())
 
@@ -557,6 +562,6 @@ def tb_moe_combine(y, weights, ids, experts: int, out, stream=None) -> None:
     fn = "tb_moe_combine"
     t, topk = _matrix_rows(fn, "ids", ids)
     code, n, dev = _dtype(fn, out), int(out.shape[-1]), ids.device
-    _check(fn, dev, y=(y, torch.float32, (t * topk, n)), weights=(weights, torch.float32, (t, topk)),
-           ids=(ids, torch.int32, (t, topk)), out=(out, out.dtype, (t, n)))
+    _check(fn, dev, ("y", y, torch.float32, (t * topk, n)), ("weights", weights, torch.float32, (t, topk)),
+           ("ids", ids, torch.int32, (t, topk)), ("out", out, out.dtype, (t, n)))
     _launch(fn, dev, stream, y.data_ptr(), weights.data_ptr(), ids.data_ptr(), t, topk, experts, n, out.data_ptr(), code)

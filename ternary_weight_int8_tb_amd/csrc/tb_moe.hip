@@ -32,6 +32,7 @@ constexpr int kXcds = 8;
 // ------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanLoads = 4;   // loads of 256 ids that a wave has in flight
 
 __global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const int32_t *__restrict__ ids, int pairs,
                                                                 int experts, int32_t *__restrict__ offsets,
@@ -39,15 +40,33 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const int32_t *_
 {
     __shared__ int less_s[kPlanWaves], same_s[kPlanWaves];
     const int e = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    // each wave takes a contiguous range of whole 64-pair groups
-    const int groups = (pairs - 1) / 64 + 1;
+    // each wave takes a contiguous range of whole groups of 256 ids, lane l ids 4 l .. 4 l + 3
+    const int groups = (pairs - 1) / 256 + 1;
     const int g0 = part_lo(groups, kPlanWaves, wave), g1 = part_lo(groups, kPlanWaves, wave + 1);
+    auto read = [&](int g, int (&id)[4]) {
+        const int64_t p = (int64_t)g * 256 + lane * 4;
+        if (g < g1 && p + 4 <= pairs) {
+            const int4 v = *reinterpret_cast<const int4 *>(ids + p);
+            id[0] = v.x, id[1] = v.y, id[2] = v.z, id[3] = v.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                id[c] = g < g1 && p + c < pairs ? ids[p + c] : -1;
+        }
+    };
     int less = 0, same = 0;
-    for (int g = g0; g < g1; ++g) {
-        const int64_t p = (int64_t)g * 64 + lane;
-        const int id = p < pairs ? ids[p] : -1;
-        less += __popcll(__ballot(id >= 0 && id < e));
-        same += __popcll(__ballot(id == e));
+    for (int g = g0; g < g1; g += kPlanLoads) {
+        int id[kPlanLoads][4];
+#pragma unroll
+        for (int x = 0; x < kPlanLoads; ++x)
+            read(g + x, id[x]);
+#pragma unroll
+        for (int x = 0; x < kPlanLoads; ++x)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                less += __popcll(__ballot((unsigned)id[x][c] < (unsigned)e));
+                same += __popcll(__ballot(id[x][c] == e));
+            }
     }
     if (lane == 0) {
         less_s[wave] = less;
@@ -61,16 +80,30 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const int32_t *_
     }
     if (threadIdx.x == 0)
         offsets[e] = start;
-    if (e == experts)
+    if (e == experts || same == 0)
         return;
     int at = start + before;
-    for (int g = g0; g < g1; ++g) {
-        const int64_t p = (int64_t)g * 64 + lane;
-        const bool mine = p < pairs && ids[p] == e;
-        const uint64_t mask = __ballot(mine);
-        if (mine)
-            order[at + __popcll(mask & ((1ull << lane) - 1))] = (int)p;
-        at += __popcll(mask);
+    const uint64_t lower = (1ull << lane) - 1;
+    for (int g = g0; g < g1; g += kPlanLoads) {
+        int id[kPlanLoads][4];
+#pragma unroll
+        for (int x = 0; x < kPlanLoads; ++x)
+            read(g + x, id[x]);
+#pragma unroll
+        for (int x = 0; x < kPlanLoads; ++x) {
+            int ahead = 0, all = 0;   // of this group: in lower lanes, and in all
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint64_t mask = __ballot(id[x][c] == e);
+                ahead += __popcll(mask & lower);
+                all += __popcll(mask);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (id[x][c] == e)
+                    order[at + ahead++] = (g + x) * 256 + lane * 4 + c;
+            at += all;
+        }
     }
 }
 
@@ -202,9 +235,12 @@ struct MoeArgs {
 // ------------------------------------------------------------------------------------
 // Stages piece `unit` (16 activations) of block u of A row `row`: lanes 8 x .. 8 x + 7 hold the pieces of
 // a block. A piece goes to the plane (block, instruction s, lane group g) whose code word it meets
-// (StepRow); planes are `pitch` rows of 16 bytes, and the odd pitch spreads the pieces over the banks.
-template <int FMT>
-__device__ __forceinline__ void stage_piece(uint8_t *lds, int pitch, int u, int row, int unit, uint4 v)
+// (StepRow), row ^ g of it. A plane has T rows of 16 bytes, T a multiple of 16: lane groups g and g + 1
+// then read the same 16 columns of banks in the halves that one LDS cycle serves, without conflict
+// (a plane of 49 rows cost a cycle of conflict for each of the reads), and the exchange within four
+// rows spreads the pieces that a wave stages.
+template <int FMT, int T>
+__device__ __forceinline__ void stage_piece(uint8_t *lds, int u, int row, int unit, uint4 v)
 {
     v4i o;
     int s, g;
@@ -220,7 +256,7 @@ __device__ __forceinline__ void stage_piece(uint8_t *lds, int pitch, int u, int 
         const uint32_t x = row_xor(s ? v.x : v.y, 1), y = row_xor(s ? v.z : v.w, 1);
         o = s ? transpose4(x, y, v.y, v.w) : transpose4(v.x, v.z, x, y);
     }
-    reinterpret_cast<v4i *>(lds)[(u * 8 + s * 4 + g) * pitch + row] = o;
+    reinterpret_cast<v4i *>(lds)[(u * 8 + s * 4 + g) * T + (row ^ g)] = o;
 }
 
 // A row of a tile's pair t
@@ -395,8 +431,7 @@ struct WideShape {
     static constexpr int kCols = TWO ? 8 * kWaves : 16 * kWaves;
     static constexpr int kPhases = Core<FMT>::kStep / 4;      // phases of a step
     static constexpr int kBlocks = 16;                        // staged at a time
-    static constexpr int kPitch = kT + 1;                     // A rows of a plane: odd, so that a pair's 64 pieces of 16 bytes spread over the banks
-    static constexpr int kActBytes = kBlocks * 8 * kPitch * 16, kDqBytes = kBlocks * kT * 4;
+    static constexpr int kActBytes = kBlocks * 8 * kT * 16, kDqBytes = kBlocks * kT * 4;
     static constexpr int kHPitch = 132;                       // floats of a row of g or u in LDS
     static constexpr int kLds = kActBytes + kDqBytes + (TWO ? 2 * kT * kHPitch * 4 : 0);
     static_assert(kLds <= 160 * 1024 && kBlocks * kT <= kThreads, "");
@@ -441,7 +476,7 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
         for (int t = 0; t < S::kPairsPerWave; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                stage_piece<FMT>(lds, S::kPitch, 8 * h + (l >> 3), pair_row(wave * S::kPairsPerWave + t), l & 7, v[t][h]);
+                stage_piece<FMT, S::kT>(lds, 8 * h + (l >> 3), pair_row(wave * S::kPairsPerWave + t), l & 7, v[t][h]);
         if (tid < S::kBlocks * S::kT)
             dq_s[tid % S::kBlocks * S::kT + pair_row(tid / S::kBlocks)] = d;
     };
@@ -463,7 +498,7 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
                 stage(step * C::kStep);
                 __syncthreads();
             }
-            const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kPitch + i;
+            const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kT + (i ^ g);
             const float *d = dq_s + u0 * S::kT + 4 * g;
             w.deal(rows.soff & 2);
 #pragma unroll
@@ -501,7 +536,7 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
                         float term[2][4];
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const v4i a0 = act[blk[b] * 8 * S::kPitch + 16 * t], a1 = act[(blk[b] * 8 + 4) * S::kPitch + 16 * t];
+                            const v4i a0 = act[blk[b] * 8 * S::kT + 16 * t], a1 = act[(blk[b] * 8 + 4) * S::kT + 16 * t];
                             v4i z = {kMagicBits, kMagicBits, kMagicBits, kMagicBits};
                             z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, wt[b][0], z, 0, 0, 0);
                             z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, wt[b][1], z, 0, 0, 0);
@@ -597,8 +632,7 @@ struct NarrowShape {
     static constexpr int kCols = TWO ? 16 * kWaves : 32 * kWaves;
     static constexpr int kPhases = Core<FMT>::kStep / 4;
     static constexpr int kBlocks = 32;                        // staged at a time
-    static constexpr int kPitch = kT + 1;
-    static constexpr int kActBytes = kBlocks * 8 * kPitch * 16, kDqBytes = kBlocks * kT * 4;
+    static constexpr int kActBytes = kBlocks * 8 * kT * 16, kDqBytes = kBlocks * kT * 4;
     static constexpr int kLds = kActBytes + kDqBytes;
 };
 
@@ -629,7 +663,7 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
         for (int tok = 0; tok < tile.rows; ++tok) {
             const size_t row = act_row<TWO>(a, tile.slot + tok);
             const uint4 v = *reinterpret_cast<const uint4 *>(a.q + row * a.k + at * kBlock + (tid & 7) * 16);
-            stage_piece<FMT>(lds, S::kPitch, u, pair_row(tok), tid & 7, v);
+            stage_piece<FMT, S::kT>(lds, u, pair_row(tok), tid & 7, v);
             if (tid < S::kBlocks)
                 reinterpret_cast<float *>(lds + S::kActBytes)[tid * S::kT + pair_row(tok)] = c0 + tid < nb ? a.dq[row * nb + c0 + tid] : 0.0f;
         }
@@ -660,7 +694,7 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
                 for (int r = 0; r < R; ++r)
                     w[j][r].deal(rows[r].soff & 2);
                 const int u0 = step % kPer * C::kStep;
-                const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kPitch + i;
+                const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kT + (i ^ g);
                 const float *d = reinterpret_cast<const float *>(lds + S::kActBytes) + u0 * S::kT + 4 * g;
                 float part0[R][NE], part1[R][NE];
 #pragma unroll
@@ -672,7 +706,7 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int x = 4 * q + 2 * h + b, blk = x ? C::kStep - x : 0;
-                            const v4i a0 = act[blk * 8 * S::kPitch], a1 = act[(blk * 8 + 4) * S::kPitch];
+                            const v4i a0 = act[blk * 8 * S::kT], a1 = act[(blk * 8 + 4) * S::kT];
 #pragma unroll
                             for (int r = 0; r < R; ++r) {
                                 const C core = w[j][r].block(blk);
@@ -747,28 +781,61 @@ __global__ __launch_bounds__(kRotThreads) void moe_rotquant_kernel(const float *
 }
 
 // out[t] = sum over j, ascending, of weights[t][j] * y[t topk + j], leaving out pairs of no expert.
+// A workgroup takes one token and up to 256 * VEC columns, VEC of them (one 16-byte load, where n
+// allows it) a thread; four pairs' loads are in flight. Bound: memory.
 template <class T>
-__device__ __forceinline__ void put(T *p, float v)
+__device__ __forceinline__ void put(T *p, const float (&v)[1])
 {
-    p->bits = (uint16_t)tbr::pack(v, 0.0f, T());
+    p->bits = (uint16_t)tbr::pack(v[0], 0.0f, T());
 }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-
+__device__ __forceinline__ void put(float *p, const float (&v)[1]) { *p = v[0]; }
 template <class T>
-__global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restrict__ y, const float *__restrict__ weights,
-                                                          const int32_t *__restrict__ ids, int tokens, int topk,
-                                                          int experts, int n, T *__restrict__ out)
+__device__ __forceinline__ void put(T *p, const float (&v)[4])
 {
-    const size_t total = (size_t)tokens * n, stride = (size_t)gridDim.x * blockDim.x;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-        const size_t t = i / n, c = i % n;
-        float s = 0.0f;
-        for (int j = 0; j < topk; ++j) {
-            const size_t p = t * topk + j;
-            if ((unsigned)ids[p] < (unsigned)experts)
-                s = fmaf(weights[p], y[p * n + c], s);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(tbr::pack(v[0], v[1], T()), tbr::pack(v[2], v[3], T()));
+}
+__device__ __forceinline__ void put(float *p, const float (&v)[4])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+constexpr int kCombineThreads = 256;
+template <class T, int VEC>
+__global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(const float *__restrict__ y, const float *__restrict__ weights,
+                                                                      const int32_t *__restrict__ ids, int64_t items, int parts,
+                                                                      int topk, int experts, int n, T *__restrict__ out)
+{
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int t = (int)(item / parts), c = ((int)(item - (int64_t)t * parts) * kCombineThreads + (int)threadIdx.x) * VEC;
+        if (c >= n)
+            continue;
+        float s[VEC] = {};
+        for (int j0 = 0; j0 < topk; j0 += 4) {
+            float v[4][VEC], w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const size_t p = (size_t)t * topk + min(j0 + j, topk - 1);
+                const bool on = j0 + j < topk && (unsigned)ids[p] < (unsigned)experts;   // the same for all lanes
+                w[j] = on ? weights[p] : 0.0f;
+#pragma unroll
+                for (int x = 0; x < VEC; ++x)
+                    v[j][x] = 0.0f;
+                if (on) {
+                    if (VEC == 4) {
+                        const float4 q = *reinterpret_cast<const float4 *>(y + p * n + c);
+                        v[j][0] = q.x, v[j][1 % VEC] = q.y, v[j][2 % VEC] = q.z, v[j][3 % VEC] = q.w;
+                    } else {
+                        v[j][0] = y[p * n + c];
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int x = 0; x < VEC; ++x)
+                    s[x] = fmaf(w[j], v[j][x], s[x]);   // a pair left out adds 0 * 0
         }
-        put(out + i, s);
+        put(out + (size_t)t * n + c, s);
     }
 }
 
@@ -829,11 +896,11 @@ int launch_product_as(const MoeArgs &a, hipStream_t stream)
         });
     }
     using S = WideShape<FMT, TWO>;
-    // a tile's row groups go to as few workgroups as leave four for each CU, so that little is
-    // staged twice and the last workgroups end together
+    // a tile's row groups go to as few workgroups as leave two for each CU: little is staged twice
+    // (at 715 tiles of 8 row groups, gate/up: 330 us in 1 part each, 349 in 2, 371 in 4, 422 in 8)
     const int64_t tiles = most_tiles(a, S::kT);
     const int nblk = (a.n + S::kCols - 1) / S::kCols;
-    const int groups = (int)std::min<int64_t>(nblk, (1024 + tiles - 1) / tiles);
+    const int groups = (int)std::min<int64_t>(nblk, (512 + tiles - 1) / tiles);
     return launch_items(tiles, groups, [&](dim3 grid, uint32_t first) {
         hipLaunchKernelGGL((moe_wide_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first, groups);
     });
@@ -844,14 +911,22 @@ int launch_product(const MoeArgs &a, int fmt, hipStream_t stream)
     return fmt == TB_FMT_TERNARY2 ? launch_product_as<TB_FMT_TERNARY2, TWO>(a, stream) : launch_product_as<TB_FMT_SIGN1, TWO>(a, stream);
 }
 
+template <class T, int VEC>
+int launch_combine_as(const float *y, const float *weights, const int32_t *ids, int tokens, int topk, int experts, int n,
+                      void *out, hipStream_t stream)
+{
+    const int parts = (n + kCombineThreads * VEC - 1) / (kCombineThreads * VEC);
+    const int64_t items = (int64_t)tokens * parts;
+    hipLaunchKernelGGL((moe_combine_kernel<T, VEC>), dim3((unsigned)std::min<int64_t>(items, kMaxGrid)), dim3(kCombineThreads), 0, stream,
+                       y, weights, ids, items, parts, topk, experts, n, static_cast<T *>(out));
+    return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
+}
 template <class T>
 int launch_combine(const float *y, const float *weights, const int32_t *ids, int tokens, int topk, int experts, int n,
                    void *out, hipStream_t stream)
 {
-    const int grid = (int)std::min<size_t>(((size_t)tokens * n + 255) / 256, kMaxGrid);
-    hipLaunchKernelGGL(moe_combine_kernel<T>, dim3(grid), dim3(256), 0, stream, y, weights, ids, tokens, topk, experts, n,
-                       static_cast<T *>(out));
-    return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
+    return n % 4 ? launch_combine_as<T, 1>(y, weights, ids, tokens, topk, experts, n, out, stream)
+                 : launch_combine_as<T, 4>(y, weights, ids, tokens, topk, experts, n, out, stream);
 }
 
 }  // namespace

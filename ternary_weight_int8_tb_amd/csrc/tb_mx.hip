@@ -177,9 +177,269 @@ __global__ __launch_bounds__(64 * kRowWaves) void mx_rows_kernel(const uint8_t *
     }
 }
 
-template <class T>
-int launch_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, T *y, hipStream_t stream)
+// ------------------------------------------------------------------------------------
+// Product, many rows. v_mfma_scale_f32_32x32x64_f8f6f4: lane (i, g) = (l % 32, l / 32) supplies one
+// 32-element block of row i of either operand, and any block of the row will do as long as A and B
+// agree. k is taken in groups of 512 (16 blocks); lane group g takes blocks 8 g .. 8 g + 7 of a group,
+// so that its 8 scales are 8 consecutive bytes, which the instruction picks one by one (opsel).
+//   * A workgroup of 4 waves makes 64 TI weight rows x 64 TJ activation rows, a wave 32 TI x 32 TJ.
+//   * Codes go from memory straight to LDS (buffer_load ... lds, 16 bytes a lane), half a group (256
+//     elements, 128 bytes a row) at a time into one of two buffers while the other is multiplied.
+//     Block j of row r lies at place j ^ ((r / 2) % 8) of the row's 8, so that the 16 lanes that one
+//     LDS cycle serves read 16 different columns of banks. A group's scales go the same way.
+// Bound: matrix rate. Per 64 elements of k a wave's TI TJ instructions take 32 TI TJ cycles and TI + TJ
+// reads of 1 KB: at 4 x 4 all four waves read 64 bytes a cycle of the 128 that LDS gives.
+// ------------------------------------------------------------------------------------
+constexpr int kGroup = 512;              // elements of k whose scales are loaded together
+constexpr uint32_t kBufWord3 = 0x00020000u;
+constexpr uint32_t kOutOfRange = 0x80000000u;   // a lane offset past every buffer: the load gives zeros
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, (int)kBufWord3);
+}
+// 16 (or 4) bytes a lane, to consecutive places from dst on; a lane whose offset is out of range
+// stores zeros
+__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t r, uint8_t *dst, uint32_t off, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, soff, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds4(__amdgpu_buffer_rsrc_t r, uint8_t *dst, uint32_t off, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 4, off, soff, 0, 0);
+}
+
+struct MxArgs {
+    const uint8_t *wc, *ws, *ac, *as;
+    int m, n, k;
+    void *y;
+    float *part;    // sums of a part of k, [parts][m][n]; null: y is written
+    int parts;
+};
+
+// All tiles of one step; S picks a byte of the scales, a constant of the instruction.
+template <int S, int TI, int TJ>
+__device__ __forceinline__ void mx_step(v16f (&acc)[TI][TJ], const uint4 (&wa)[TI], const uint4 (&xb)[TJ], const u32x2 (&sa)[TI],
+                                        const u32x2 (&sb)[TJ], int q)
+{
+#pragma unroll
+    for (int ti = 0; ti < TI; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TJ; ++tj)
+            acc[ti][tj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(wa[ti]), operand(xb[tj]), acc[ti][tj], 4, 4, S,
+                                                                          (int)sa[ti][q], S, (int)sb[tj][q]);
+    // the instructions are pure: held here, or they sink below the next barrier
+#pragma unroll
+    for (int ti = 0; ti < TI; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TJ; ++tj)
+            asm volatile("" : "+a"(acc[ti][tj]));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int TI, int TJ, class T>
+__global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
+{
+    constexpr int kRows = 64 * (TI + TJ);   // weight rows, then activation rows
+    __shared__ __align__(16) uint8_t buf0[kRows * 128];
+    __shared__ __align__(16) uint8_t buf1[kRows * 128];
+    __shared__ __align__(16) uint8_t sbuf[kRows * 16];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 31, g = l >> 5;
+    const int wi = wave & 1, wj = wave >> 1;
+    const int ntn = (a.n + 64 * TI - 1) / (64 * TI), ntm = (a.m + 64 * TJ - 1) / (64 * TJ);
+    // tiles in blocks of 8 along n, dealt to the XCDs in contiguous ranges (workgroup b runs on XCD
+    // b % 8): the tiles that run on an XCD at a time share their rows in its L2
+    const int tiles = ntn * ntm, per = (tiles + 7) / 8, b = blockIdx.x, item = (b % 8) * per + b / 8;
+    if (b / 8 >= per || item >= tiles)
+        return;
+    const int band = item / (8 * ntm), width = min(8, ntn - band * 8), r = item - band * 8 * ntm;
+    const int n0 = (band * 8 + r % width) * 64 * TI, m0 = r / width * 64 * TJ;
+    const int kb = a.k / kMxBlock, groups = (kb + 15) / 16;
+    const int part = blockIdx.y, g0 = (int)((long long)groups * part / a.parts), g1 = (int)((long long)groups * (part + 1) / a.parts);
+    const int pitch = a.k / 2, spitch = kb;
+
+    // staging: a wave takes 8 rows at a time, lane l place l % 8 of row l / 8; rows past the end are
+    // the last one, and what they give is not stored
+    constexpr int kLoads = kRows / 32;
+    const __amdgpu_buffer_rsrc_t wr = buffer(a.wc + (size_t)n0 * pitch, (uint32_t)(min(a.n - n0, 64 * TI) * pitch));
+    const __amdgpu_buffer_rsrc_t ar = buffer(a.ac + (size_t)m0 * pitch, (uint32_t)(min(a.m - m0, 64 * TJ) * pitch));
+    const __amdgpu_buffer_rsrc_t wsr = buffer(a.ws + (size_t)n0 * spitch, (uint32_t)(min(a.n - n0, 64 * TI) * spitch));
+    const __amdgpu_buffer_rsrc_t asr = buffer(a.as + (size_t)m0 * spitch, (uint32_t)(min(a.m - m0, 64 * TJ) * spitch));
+    const int j = (l & 7) ^ ((wave & 1) * 4 + (l >> 4));   // the lane's block of the half group
+    const int jblock = 8 * (j >> 2) + (j & 3);             // and of the group (first half)
+    uint32_t off[kLoads];
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+        const int row = x * 32 + wave * 8 + (l >> 3);
+        off[x] = (x < 2 * TI ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * pitch + jblock * 16;
+    }
+    auto load = [&](uint8_t *buf, int grp, int q) {   // half q of a group
+        const bool none = grp * 16 + q * 4 + jblock >= kb;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x)
+            load_to_lds16(x < 2 * TI ? wr : ar, buf + (x * 32 + wave * 8) * 128, none ? kOutOfRange : off[x], grp * 256 + q * 64);
+    };
+    // 16 bytes of a row a lane; of a last group that is not full, word by word, as the row's end allows
+    auto load_scales = [&](uint8_t *buf, int grp) {
+        if (grp * 16 + 16 <= kb) {
+#pragma unroll
+            for (int x = 0; x < kRows / 256; ++x) {
+                const int row = x * 256 + tid;
+                const bool w = x * 256 + wave * 64 < 64 * TI;   // the same for all lanes
+                load_to_lds16(w ? wsr : asr, buf + (x * 256 + wave * 64) * 16,
+                                (w ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * spitch, grp * 16);
+            }
+        } else {
+            for (int x = 0; x < kRows / 64; ++x) {
+                const int row = x * 64 + (tid >> 2), word = tid & 3;
+                const bool w = x < TI;
+                load_to_lds4(w ? wsr : asr, buf + (x * 64 + wave * 16) * 16,
+                               grp * 16 + word * 4 >= kb ? kOutOfRange
+                                                         : (w ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * spitch + word * 4,
+                               grp * 16);
+            }
+        }
+    };
+
+    v16f acc[TI][TJ];
+#pragma unroll
+    for (int ti = 0; ti < TI; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TJ; ++tj)
+            acc[ti][tj] = v16f{};
+    u32x2 sa[TI], sb[TJ];
+    auto read_scales = [&](const uint8_t *buf) {
+#pragma unroll
+        for (int ti = 0; ti < TI; ++ti)
+            sa[ti] = *reinterpret_cast<const u32x2 *>(buf + (wi * 32 * TI + ti * 32 + i) * 16 + g * 8);
+#pragma unroll
+        for (int tj = 0; tj < TJ; ++tj)
+            sb[tj] = *reinterpret_cast<const u32x2 *>(buf + (64 * TI + wj * 32 * TJ + tj * 32 + i) * 16 + g * 8);
+    };
+    const int wrow = (wi * 32 * TI + i) * 128, arow = (64 * TI + wj * 32 * TJ + i) * 128, swz = (i >> 1) & 7;
+    uint4 wa[2][TI], xb[2][TJ];   // operands of a step, and of the next while it is multiplied
+    auto operands = [&](const uint8_t *buf, int s) {
+        const int place = ((4 * g + s) ^ swz) * 16;
+#pragma unroll
+        for (int ti = 0; ti < TI; ++ti)
+            wa[s & 1][ti] = *reinterpret_cast<const uint4 *>(buf + wrow + ti * 4096 + place);
+#pragma unroll
+        for (int tj = 0; tj < TJ; ++tj)
+            xb[s & 1][tj] = *reinterpret_cast<const uint4 *>(buf + arow + tj * 4096 + place);
+    };
+    auto multiply = [&](const uint8_t *buf, int q) {
+        operands(buf, 0);
+        operands(buf, 1);
+        mx_step<0>(acc, wa[0], xb[0], sa, sb, q);
+        operands(buf, 2);
+        mx_step<1>(acc, wa[1], xb[1], sa, sb, q);
+        operands(buf, 3);
+        mx_step<2>(acc, wa[0], xb[0], sa, sb, q);
+        mx_step<3>(acc, wa[1], xb[1], sa, sb, q);
+    };
+
+    load(buf0, g0, 0);
+    load_scales(sbuf, g0);
+    for (int grp = g0; grp < g1; ++grp) {
+        __syncthreads();   // the first half and the scales have arrived, and buf1 has been read
+        load(buf1, grp, 1);
+        read_scales(sbuf);
+        multiply(buf0, 0);
+        __syncthreads();   // the second half has arrived, and buf0 and the scales have been read
+        if (grp + 1 < g1) {
+            load(buf0, grp + 1, 0);
+            load_scales(sbuf, grp + 1);
+        }
+        multiply(buf1, 1);
+    }
+
+    // lane l has, of each 32 x 32 tile, weight rows 8 v + 4 g + 0 .. 3 (v = 0 .. 3) of activation row l % 32
+#pragma unroll
+    for (int tj = 0; tj < TJ; ++tj) {
+        const int row = m0 + wj * 32 * TJ + tj * 32 + i;
+        if (row >= a.m)
+            continue;
+#pragma unroll
+        for (int ti = 0; ti < TI; ++ti)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int col = n0 + wi * 32 * TI + ti * 32 + 8 * v + 4 * g;
+                if (col >= a.n)
+                    continue;
+                const float o[4] = {acc[ti][tj][4 * v], acc[ti][tj][4 * v + 1], acc[ti][tj][4 * v + 2], acc[ti][tj][4 * v + 3]};
+                if (a.part)
+                    put4(a.part + ((size_t)part * a.m + row) * a.n + col, o, min(4, a.n - col));
+                else
+                    put4(static_cast<T *>(a.y) + (size_t)row * a.n + col, o, min(4, a.n - col));
+            }
+    }
+}
+
+// y = the sum of the parts, in order.
+template <class T>
+__global__ __launch_bounds__(256) void mx_sum_kernel(const float *__restrict__ part, size_t count, int parts, T *__restrict__ y)
+{
+    const size_t stride = (size_t)gridDim.x * 256 * 4;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < count; i += stride) {
+        const int c = (int)(count - i < 4 ? count - i : 4);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < parts; ++p) {
+            const float *q = part + (size_t)p * count + i;
+            if (c == 4 && ((uintptr_t)q & 15) == 0) {
+                const float4 x = *reinterpret_cast<const float4 *>(q);
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+            } else {
+                for (int e = 0; e < c; ++e)
+                    v[e] += q[e];
+            }
+        }
+        put4(y + i, v, c);
+    }
+}
+
+// How a product is run: few rows (mx_rows_kernel), or tiles of 64 t x 64 t, k in `parts`.
+struct MxPlan {
+    int t, parts;
+};
+constexpr int kRowsMost = 64;
+MxPlan plan_gemm(int m, int n, int k)
+{
+    if (m <= kRowsMost)
+        return {0, 1};
+    const int64_t big = (int64_t)((m + 255) / 256) * ((n + 255) / 256);
+    if (big >= 192)
+        return {4, 1};
+    const int64_t small = (int64_t)((m + 127) / 128) * ((n + 127) / 128);
+    const int groups = (k + kGroup - 1) / kGroup;
+    const int parts = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / small), std::max(1, groups / 2));
+    return {2, parts};
+}
+
+template <class T>
+int launch_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, T *y, float *part, hipStream_t stream)
+{
+    const MxPlan plan = plan_gemm(m, w->n, w->k);
+    if (plan.t) {
+        const int side = 64 * plan.t;
+        const int64_t tiles = (int64_t)((m + side - 1) / side) * ((w->n + side - 1) / side);
+        const dim3 grid((unsigned)((tiles + 7) / 8 * 8), plan.parts);
+        const MxArgs a = {w->codes, w->scales, codes, scales, m, w->n, w->k, y, plan.parts > 1 ? part : nullptr, plan.parts};
+        if (plan.t == 4)
+            hipLaunchKernelGGL((mx_tile_kernel<4, 4, T>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((mx_tile_kernel<2, 2, T>), grid, dim3(256), 0, stream, a);
+        if (hipGetLastError() != hipSuccess)
+            return TB_EHIP;
+        if (plan.parts > 1) {
+            const size_t count = (size_t)m * w->n;
+            hipLaunchKernelGGL(mx_sum_kernel<T>, dim3((unsigned)std::min<size_t>((count + 1023) / 1024, kMaxGrid)), dim3(256), 0, stream,
+                               part, count, plan.parts, y);
+        }
+        return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
+    }
     const int waves = std::min(kRowWaves, w->k / kBlock);
     const int mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
     const int per = 65535 * 16 * mt;   // activation rows of one launch (grid.y)
@@ -269,9 +529,10 @@ int tb_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int m, int k, 
 
 size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m)
 {
-    (void)w;
-    (void)m;
-    return 0;
+    if (!mx_ok(w) || m < 1)
+        return 0;
+    const MxPlan plan = plan_gemm(m, w->n, w->k);
+    return plan.parts > 1 ? (size_t)plan.parts * m * w->n * 4 : 0;
 }
 
 int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, void *y, int dtype, void *ws,
@@ -280,6 +541,9 @@ int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales
     const size_t eb = tbh::dtype_bytes(dtype);
     if (!eb || !mx_ok(w) || m < 1)
         return TB_EINVAL;
+    // lane offsets within a tile's rows, and the tiles of a launch, in 31 bits
+    if ((int64_t)w->k * 128 > 0x7fffffff || (int64_t)((m + 127) / 128) * ((w->n + 127) / 128) > (1 << 23))
+        return TB_EUNSUPPORTED;
     const size_t need = tb_mxfp4_gemm_workspace_bytes(w, m);
     const tbh::Arg a[] = {{w->codes, code_bytes(w->n, w->k), false},
                           {w->scales, scale_bytes(w->n, w->k), false},
@@ -293,9 +557,9 @@ int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales
         return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     switch (dtype) {
-    case TB_F32: return launch_gemm(w, codes, scales, m, static_cast<float *>(y), st);
-    case TB_BF16: return launch_gemm(w, codes, scales, m, static_cast<Bf16 *>(y), st);
-    default: return launch_gemm(w, codes, scales, m, static_cast<F16 *>(y), st);
+    case TB_F32: return launch_gemm(w, codes, scales, m, static_cast<float *>(y), static_cast<float *>(ws), st);
+    case TB_BF16: return launch_gemm(w, codes, scales, m, static_cast<Bf16 *>(y), static_cast<float *>(ws), st);
+    default: return launch_gemm(w, codes, scales, m, static_cast<F16 *>(y), static_cast<float *>(ws), st);
     }
 }
 
