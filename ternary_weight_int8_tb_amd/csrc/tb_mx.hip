@@ -244,6 +244,7 @@ template <int TI, int TJ, class T>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
 {
     constexpr int kRows = 64 * (TI + TJ);   // weight rows, then activation rows
+    // two buffers of codes, arrays of their own: a read of one then waits for no load of the other
     __shared__ __align__(16) uint8_t buf0[kRows * 128];
     __shared__ __align__(16) uint8_t buf1[kRows * 128];
     __shared__ __align__(16) uint8_t sbuf[kRows * 16];
@@ -356,25 +357,36 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
         multiply(buf1, 1);
     }
 
-    // lane l has, of each 32 x 32 tile, weight rows 8 v + 4 g + 0 .. 3 (v = 0 .. 3) of activation row l % 32
+    // Lane l has, of each 32 x 32 tile, weight rows 8 v + 4 g + 0 .. 3 (v = 0 .. 3) of activation row
+    // l % 32. Stored so, a row would be written 8 or 16 bytes at a time; a wave passes 32 rows at a
+    // time through its part of LDS instead and writes whole lines.
+    // (Place c ^ r of row r for its 16-byte column c: no bank conflicts.)
+    constexpr int kLanes = 8 * TI, kPer = 64 / kLanes;   // lanes of a row, rows of a store
+    static_assert(4 * 32 * kLanes * 16 <= kRows * 128, "the waves' rows take a code buffer");
+    float4 *mine = reinterpret_cast<float4 *>(buf0) + wave * 32 * kLanes;
+    const int col = n0 + wi * 32 * TI + l % kLanes * 4;
+    __syncthreads();
 #pragma unroll
     for (int tj = 0; tj < TJ; ++tj) {
-        const int row = m0 + wj * 32 * TJ + tj * 32 + i;
-        if (row >= a.m)
-            continue;
 #pragma unroll
         for (int ti = 0; ti < TI; ++ti)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int col = n0 + wi * 32 * TI + ti * 32 + 8 * v + 4 * g;
-                if (col >= a.n)
-                    continue;
-                const float o[4] = {acc[ti][tj][4 * v], acc[ti][tj][4 * v + 1], acc[ti][tj][4 * v + 2], acc[ti][tj][4 * v + 3]};
+            for (int v = 0; v < 4; ++v)
+                mine[i * kLanes + ((ti * 8 + 2 * v + g) ^ (i % kLanes))] =
+                    make_float4(acc[ti][tj][4 * v], acc[ti][tj][4 * v + 1], acc[ti][tj][4 * v + 2], acc[ti][tj][4 * v + 3]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // a wave reads what its own lanes wrote
+        for (int x = 0; x < 32 / kPer; ++x) {
+            const int r = x * kPer + l / kLanes, row = m0 + wj * 32 * TJ + tj * 32 + r;
+            const float4 o = mine[r * kLanes + (l % kLanes ^ r % kLanes)];
+            if (row < a.m && col < a.n) {
+                const float f[4] = {o.x, o.y, o.z, o.w};
                 if (a.part)
-                    put4(a.part + ((size_t)part * a.m + row) * a.n + col, o, min(4, a.n - col));
+                    put4(a.part + ((size_t)part * a.m + row) * a.n + col, f, min(4, a.n - col));
                 else
-                    put4(static_cast<T *>(a.y) + (size_t)row * a.n + col, o, min(4, a.n - col));
+                    put4(static_cast<T *>(a.y) + (size_t)row * a.n + col, f, min(4, a.n - col));
             }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
