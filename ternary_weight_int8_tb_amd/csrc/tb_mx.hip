@@ -180,8 +180,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void mx_rows_kernel(const uint8_t *
 // ------------------------------------------------------------------------------------
 // Product, many rows. v_mfma_scale_f32_32x32x64_f8f6f4: lane (i, g) = (l % 32, l / 32) supplies one
 // 32-element block of row i of either operand, and any block of the row will do as long as A and B
-// agree. k is taken in groups of 512 (16 blocks); lane group g takes blocks 8 g .. 8 g + 7 of a group,
-// so that its 8 scales are 8 consecutive bytes, which the instruction picks one by one (opsel).
+// agree. k is taken in halves of 256 (8 blocks, a 128-byte line of codes); lane group g takes blocks
+// 4 g .. 4 g + 3 of a half, so that its scales are one word, whose bytes the instruction picks one by
+// one (opsel). Two halves are a group, whose scales are loaded together.
 //   * A workgroup of 4 waves makes 64 TI weight rows x 64 TJ activation rows, a wave 32 TI x 32 TJ.
 //   * Codes go from memory straight to LDS (buffer_load ... lds, 16 bytes a lane), half a group (256
 //     elements, 128 bytes a row) at a time into one of two buffers while the other is multiplied.
@@ -195,7 +196,6 @@ constexpr uint32_t kBufWord3 = 0x00020000u;
 constexpr uint32_t kOutOfRange = 0x80000000u;   // a lane offset past every buffer: the load gives zeros
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
@@ -220,24 +220,25 @@ struct MxArgs {
     int parts;
 };
 
-// All tiles of one step; S picks a byte of the scales, a constant of the instruction.
-template <int S, int TI, int TJ>
-__device__ __forceinline__ void mx_step(v16f (&acc)[TI][TJ], const uint4 (&wa)[TI], const uint4 (&xb)[TJ], const u32x2 (&sa)[TI],
-                                        const u32x2 (&sb)[TJ], int q)
+// All tiles of one step; S picks a byte of the scales, a constant of the instruction. After each row of
+// tiles `also(ti)` issues its share of the next step's reads and of the next half's loads: a wave
+// issues in order, and waits behind a burst of either with nothing to multiply.
+template <int S, int TI, int TJ, class F>
+__device__ __forceinline__ void mx_step(v16f (&acc)[TI][TJ], const uint4 (&wa)[TI], const uint4 (&xb)[TJ], const uint32_t (&sa)[TI][2],
+                                        const uint32_t (&sb)[TJ][2], int q, F &&also)
 {
 #pragma unroll
-    for (int ti = 0; ti < TI; ++ti)
+    for (int ti = 0; ti < TI; ++ti) {
 #pragma unroll
-        for (int tj = 0; tj < TJ; ++tj)
+        for (int tj = 0; tj < TJ; ++tj) {
             acc[ti][tj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(wa[ti]), operand(xb[tj]), acc[ti][tj], 4, 4, S,
                                                                           (int)sa[ti][q], S, (int)sb[tj][q]);
-    // the instructions are pure: held here, or they sink below the next barrier
-#pragma unroll
-    for (int ti = 0; ti < TI; ++ti)
-#pragma unroll
-        for (int tj = 0; tj < TJ; ++tj)
+            // the instructions are pure: held here, or they sink below the next barrier
             asm volatile("" : "+a"(acc[ti][tj]));
-    __builtin_amdgcn_sched_barrier(0);
+        }
+        also(ti);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 template <int TI, int TJ, class T>
@@ -270,18 +271,16 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     const __amdgpu_buffer_rsrc_t wsr = buffer(a.ws + (size_t)n0 * spitch, (uint32_t)(min(a.n - n0, 64 * TI) * spitch));
     const __amdgpu_buffer_rsrc_t asr = buffer(a.as + (size_t)m0 * spitch, (uint32_t)(min(a.m - m0, 64 * TJ) * spitch));
     const int j = (l & 7) ^ ((wave & 1) * 4 + (l >> 4));   // the lane's block of the half group
-    const int jblock = 8 * (j >> 2) + (j & 3);             // and of the group (first half)
     uint32_t off[kLoads];
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
         const int row = x * 32 + wave * 8 + (l >> 3);
-        off[x] = (x < 2 * TI ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * pitch + jblock * 16;
+        off[x] = (x < 2 * TI ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * pitch + j * 16;
     }
-    auto load = [&](uint8_t *buf, int grp, int q) {   // half q of a group
-        const bool none = grp * 16 + q * 4 + jblock >= kb;
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x)
-            load_to_lds16(x < 2 * TI ? wr : ar, buf + (x * 32 + wave * 8) * 128, none ? kOutOfRange : off[x], grp * 256 + q * 64);
+    static_assert(TI == TJ && kLoads == 4 * TI, "two loads and two reads for each row of a step");
+    auto load = [&](uint8_t *buf, int grp, int q, int x) {   // load x of half q of a group
+        const bool none = grp * 16 + q * 8 + j >= kb;
+        load_to_lds16(x < 2 * TI ? wr : ar, buf + (x * 32 + wave * 8) * 128, none ? kOutOfRange : off[x], grp * 256 + q * 128);
     };
     // 16 bytes of a row a lane; of a last group that is not full, word by word, as the row's end allows
     auto load_scales = [&](uint8_t *buf, int grp) {
@@ -311,50 +310,77 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
 #pragma unroll
         for (int tj = 0; tj < TJ; ++tj)
             acc[ti][tj] = v16f{};
-    u32x2 sa[TI], sb[TJ];
-    auto read_scales = [&](const uint8_t *buf) {
+    uint32_t sa[TI][2], sb[TJ][2], na[TI][2], nb[TJ][2];   // scales of a group, and of the next
+    auto read_scales = [&](uint32_t (&xa)[TI][2], uint32_t (&xb)[TJ][2]) {
 #pragma unroll
-        for (int ti = 0; ti < TI; ++ti)
-            sa[ti] = *reinterpret_cast<const u32x2 *>(buf + (wi * 32 * TI + ti * 32 + i) * 16 + g * 8);
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int tj = 0; tj < TJ; ++tj)
-            sb[tj] = *reinterpret_cast<const u32x2 *>(buf + (64 * TI + wj * 32 * TJ + tj * 32 + i) * 16 + g * 8);
+            for (int ti = 0; ti < TI; ++ti)
+                xa[ti][q] = *reinterpret_cast<const uint32_t *>(sbuf + (wi * 32 * TI + ti * 32 + i) * 16 + q * 8 + g * 4);
+#pragma unroll
+            for (int tj = 0; tj < TJ; ++tj)
+                xb[tj][q] = *reinterpret_cast<const uint32_t *>(sbuf + (64 * TI + wj * 32 * TJ + tj * 32 + i) * 16 + q * 8 + g * 4);
+        }
     };
     const int wrow = (wi * 32 * TI + i) * 128, arow = (64 * TI + wj * 32 * TJ + i) * 128, swz = (i >> 1) & 7;
     uint4 wa[2][TI], xb[2][TJ];   // operands of a step, and of the next while it is multiplied
-    auto operands = [&](const uint8_t *buf, int s) {
+    auto operand_pair = [&](const uint8_t *buf, int s, int t) {
         const int place = ((4 * g + s) ^ swz) * 16;
-#pragma unroll
-        for (int ti = 0; ti < TI; ++ti)
-            wa[s & 1][ti] = *reinterpret_cast<const uint4 *>(buf + wrow + ti * 4096 + place);
-#pragma unroll
-        for (int tj = 0; tj < TJ; ++tj)
-            xb[s & 1][tj] = *reinterpret_cast<const uint4 *>(buf + arow + tj * 4096 + place);
+        wa[s & 1][t] = *reinterpret_cast<const uint4 *>(buf + wrow + t * 4096 + place);
+        xb[s & 1][t] = *reinterpret_cast<const uint4 *>(buf + arow + t * 4096 + place);
     };
-    auto multiply = [&](const uint8_t *buf, int q) {
-        operands(buf, 0);
-        operands(buf, 1);
-        mx_step<0>(acc, wa[0], xb[0], sa, sb, q);
-        operands(buf, 2);
-        mx_step<1>(acc, wa[1], xb[1], sa, sb, q);
-        operands(buf, 3);
-        mx_step<2>(acc, wa[0], xb[0], sa, sb, q);
-        mx_step<3>(acc, wa[1], xb[1], sa, sb, q);
+    // Half q from `buf`, whose first step's operands are read. Loads of the next half into `next` were
+    // begun by the last step before; the loads after that go to `buf` from the barrier on, where
+    // every wave has read it. So a half's loads have two steps to arrive in after the last is issued.
+    auto multiply = [&](uint8_t *buf, uint8_t *next, int q, int grp) {
+        const int ngrp = q ? grp + 1 : grp;   // of the next half
+        mx_step<0>(acc, wa[0], xb[0], sa, sb, q, [&](int ti) {
+            operand_pair(buf, 1, ti);
+            if (ngrp < g1) {
+                load(next, ngrp, 1 - q, 2 * TI + 2 * ti);
+                load(next, ngrp, 1 - q, 2 * TI + 2 * ti + 1);
+            }
+        });
+        if (q && ngrp < g1)
+            load_scales(sbuf, ngrp);
+        mx_step<1>(acc, wa[1], xb[1], sa, sb, q, [&](int ti) { operand_pair(buf, 2, ti); });
+        mx_step<2>(acc, wa[0], xb[0], sa, sb, q, [&](int ti) { operand_pair(buf, 3, ti); });
+        __syncthreads();   // the next half (and its scales) have arrived, and buf has been read
+        if (q)
+            read_scales(na, nb);
+        mx_step<3>(acc, wa[1], xb[1], sa, sb, q, [&](int ti) {
+            operand_pair(next, 0, ti);
+            if (grp + 1 < g1) {
+                load(buf, grp + 1, q, 2 * ti);
+                load(buf, grp + 1, q, 2 * ti + 1);
+            }
+        });
     };
 
-    load(buf0, g0, 0);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x)
+        load(buf0, g0, 0, x);
     load_scales(sbuf, g0);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2 * TI; ++x)
+        load(buf1, g0, 1, x);
+    read_scales(sa, sb);
+#pragma unroll
+    for (int t = 0; t < TI; ++t)
+        operand_pair(buf0, 0, t);
     for (int grp = g0; grp < g1; ++grp) {
-        __syncthreads();   // the first half and the scales have arrived, and buf1 has been read
-        load(buf1, grp, 1);
-        read_scales(sbuf);
-        multiply(buf0, 0);
-        __syncthreads();   // the second half has arrived, and buf0 and the scales have been read
-        if (grp + 1 < g1) {
-            load(buf0, grp + 1, 0);
-            load_scales(sbuf, grp + 1);
+        multiply(buf0, buf1, 0, grp);
+        multiply(buf1, buf0, 1, grp);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int ti = 0; ti < TI; ++ti)
+                sa[ti][q] = na[ti][q];
+#pragma unroll
+            for (int tj = 0; tj < TJ; ++tj)
+                sb[tj][q] = nb[tj][q];
         }
-        multiply(buf1, 1);
     }
 
     // Lane l has, of each 32 x 32 tile, weight rows 8 v + 4 g + 0 .. 3 (v = 0 .. 3) of activation row
