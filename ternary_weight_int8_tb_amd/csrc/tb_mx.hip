@@ -94,11 +94,14 @@ __global__ __launch_bounds__(kQuantThreads) void mx_dequant_kernel(const uint32_
 
 // ------------------------------------------------------------------------------------
 // Product, few rows. v_mfma_scale_f32_16x16x128_f8f6f4: lane (i, g) = (lane % 16, lane / 16)
-// supplies the 32 codes (16 bytes) and the scale of block g of row i, for A and B alike; lane l
-// ends with rows 4 g + 0 .. 3 of A against row l % 16 of B. A is the weights, B the activation, so
-// an operand of either is one 16-byte load from its row, with no exchange and no LDS.
-// A workgroup owns 16 weight rows and 16 * MT activation rows; its waves split k, and add their
-// sums through LDS in wave order: the order depends on (n, k) alone.
+// supplies 32 codes (16 bytes) of one block of row i and their scale, for A and B alike, of any
+// block as long as both agree; lane l ends with rows 4 g + 0 .. 3 of A against row l % 16 of B. A is
+// the weights, B the activation, so an operand of either comes from its row, with no exchange and no
+// LDS. k goes in halves of 256 elements, a 128-byte line of codes; lane group g takes blocks 2 g and
+// 2 g + 1 of a half, whose two scales are one 16-bit load.
+// A workgroup owns 16 weight rows and all (up to 16) activation rows; its waves split k, and add their
+// sums through LDS in wave order: the order depends on k alone. Bound: the weights' way from
+// memory; a wave has the loads of U halves in flight at a time.
 // ------------------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 
@@ -125,55 +128,68 @@ __device__ __forceinline__ void put4(T *p, const float (&v)[4], int count)
     }
 }
 
-template <int MT, class T>
+// A lane's share of a half of its row.
+struct Half {
+    uint4 c[2];
+    int scale;   // of both blocks, a byte each
+    // codes, scales: the row's, from the lane's first block on; blocks past the row's kb are zeros
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, int h, int kb, int g)
+    {
+        if ((h + 1) * 8 <= kb || h * 8 + 2 * g < kb) {
+            c[0] = *reinterpret_cast<const uint4 *>(codes + (size_t)h * 128);
+            c[1] = *reinterpret_cast<const uint4 *>(codes + (size_t)h * 128 + 16);
+            scale = *reinterpret_cast<const uint16_t *>(scales + (size_t)h * 8);
+        } else {
+            c[0] = c[1] = make_uint4(0, 0, 0, 0);
+            scale = 0x7f7f;
+        }
+    }
+};
+
+template <class T>
 __global__ __launch_bounds__(64 * kRowWaves) void mx_rows_kernel(const uint8_t *__restrict__ wc,
                                                                  const uint8_t *__restrict__ ws,
                                                                  const uint8_t *__restrict__ ac,
                                                                  const uint8_t *__restrict__ as, int m, int n, int k,
                                                                  T *__restrict__ y)
 {
-    __shared__ float4 part[kRowWaves][MT][64];
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, i = l & 15, g = l >> 4;
-    const int waves = blockDim.x >> 6, steps = k / kBlock;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
-    const int s0 = (int)((long long)steps * wave / waves), s1 = (int)((long long)steps * (wave + 1) / waves);
+    constexpr int U = 4;   // halves in flight
+    __shared__ float4 part[kRowWaves][64];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 15, g = l >> 4;
+    const int waves = blockDim.x >> 6, kb = k / kMxBlock, halves = (kb + 7) / 8;
+    const int n0 = blockIdx.x * 16;
+    const int h0 = halves * wave / waves, h1 = halves * (wave + 1) / waves;
     // rows past the end read the last one; what they give is not stored
-    const size_t jr = min(n0 + i, n - 1);
-    const uint8_t *pc = wc + jr * (k / 2) + g * 16, *ps = ws + jr * (k / kMxBlock) + g;
-    const uint8_t *qc[MT], *qs[MT];
-    v4f acc[MT];
+    const size_t jr = min(n0 + i, n - 1), r = min(i, m - 1);
+    const uint8_t *pc = wc + jr * (k / 2) + g * 32, *ps = ws + jr * kb + g * 2;
+    const uint8_t *qc = ac + r * (k / 2) + g * 32, *qs = as + r * kb + g * 2;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    for (int h = h0; h < h1; h += U) {
+        Half a[U], b[U];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const size_t r = min(m0 + t * 16 + i, m - 1);
-        qc[t] = ac + r * (k / 2) + g * 16;
-        qs[t] = as + r * (k / kMxBlock) + g;
-        acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < U; ++u)
+            if (h + u < h1) {   // the same for all lanes
+                a[u].load(pc, ps, h + u, kb, g);
+                b[u].load(qc, qs, h + u, kb, g);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h + u < h1) {
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a[u].c[0]), operand(b[u].c[0]), acc, 4, 4, 0, a[u].scale, 0, b[u].scale);
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a[u].c[1]), operand(b[u].c[1]), acc, 4, 4, 1, a[u].scale, 1, b[u].scale);
+            }
     }
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-        const v8i a = operand(*reinterpret_cast<const uint4 *>(pc + (size_t)s * 64));
-        const int sa = ps[s * 4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const v8i b = operand(*reinterpret_cast<const uint4 *>(qc[t] + (size_t)s * 64));
-            const int sb = qs[t][s * 4];
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[t], 4, 4, 0, sa, 0, sb);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        part[wave][t][l] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    part[wave][l] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
-    for (int u = tid; u < MT * 64; u += blockDim.x) {
-        const int t = u >> 6, ul = u & 63;
+    if (wave == 0) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         for (int w = 0; w < waves; ++w) {
-            const float4 p = part[w][t][ul];
+            const float4 p = part[w][l];
             v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
         }
-        const int r = m0 + t * 16 + (ul & 15), j = n0 + 4 * (ul >> 4);
-        if (r < m && j < n)
-            put4(y + (size_t)r * n + j, v, min(4, n - j));
+        const int j = n0 + 4 * g;
+        if (i < m && j < n)
+            put4(y + (size_t)i * n + j, v, min(4, n - j));
     }
 }
 
@@ -277,7 +293,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
         const int row = x * 32 + wave * 8 + (l >> 3);
         off[x] = (x < 2 * TI ? min(row, a.n - n0 - 1) : min(row - 64 * TI, a.m - m0 - 1)) * pitch + j * 16;
     }
-    static_assert(TI == TJ && kLoads == 4 * TI, "two loads and two reads for each row of a step");
+    static_assert(kLoads == 2 * (TI + TJ) && TJ <= TI, "half of the loads, and all reads, in the TI rows of a step");
     auto load = [&](uint8_t *buf, int grp, int q, int x) {   // load x of half q of a group
         const bool none = grp * 16 + q * 8 + j >= kb;
         load_to_lds16(x < 2 * TI ? wr : ar, buf + (x * 32 + wave * 8) * 128, none ? kOutOfRange : off[x], grp * 256 + q * 128);
@@ -286,7 +302,9 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     auto load_scales = [&](uint8_t *buf, int grp) {
         if (grp * 16 + 16 <= kb) {
 #pragma unroll
-            for (int x = 0; x < kRows / 256; ++x) {
+            for (int x = 0; x < (kRows + 255) / 256; ++x) {
+                if (kRows % 256 && x * 256 + wave * 64 >= kRows)
+                    continue;
                 const int row = x * 256 + tid;
                 const bool w = x * 256 + wave * 64 < 64 * TI;   // the same for all lanes
                 load_to_lds16(w ? wsr : asr, buf + (x * 256 + wave * 64) * 16,
@@ -327,7 +345,14 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     auto operand_pair = [&](const uint8_t *buf, int s, int t) {
         const int place = ((4 * g + s) ^ swz) * 16;
         wa[s & 1][t] = *reinterpret_cast<const uint4 *>(buf + wrow + t * 4096 + place);
-        xb[s & 1][t] = *reinterpret_cast<const uint4 *>(buf + arow + t * 4096 + place);
+        if (t < TJ)
+            xb[s & 1][t] = *reinterpret_cast<const uint4 *>(buf + arow + t * 4096 + place);
+    };
+    // row ti's share of the first (from = 0) or second half of a half group's loads
+    auto load_share = [&](uint8_t *buf, int grp, int q, int from, int ti) {
+#pragma unroll
+        for (int x = (TI + TJ) * ti / TI; x < (TI + TJ) * (ti + 1) / TI; ++x)
+            load(buf, grp, q, from * (TI + TJ) + x);
     };
     // Half q from `buf`, whose first step's operands are read. Loads of the next half into `next` were
     // begun by the last step before; the loads after that go to `buf` from the barrier on, where
@@ -336,10 +361,8 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
         const int ngrp = q ? grp + 1 : grp;   // of the next half
         mx_step<0>(acc, wa[0], xb[0], sa, sb, q, [&](int ti) {
             operand_pair(buf, 1, ti);
-            if (ngrp < g1) {
-                load(next, ngrp, 1 - q, 2 * TI + 2 * ti);
-                load(next, ngrp, 1 - q, 2 * TI + 2 * ti + 1);
-            }
+            if (ngrp < g1)
+                load_share(next, ngrp, 1 - q, 1, ti);
         });
         if (q && ngrp < g1)
             load_scales(sbuf, ngrp);
@@ -350,10 +373,8 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
             read_scales(na, nb);
         mx_step<3>(acc, wa[1], xb[1], sa, sb, q, [&](int ti) {
             operand_pair(next, 0, ti);
-            if (grp + 1 < g1) {
-                load(buf, grp + 1, q, 2 * ti);
-                load(buf, grp + 1, q, 2 * ti + 1);
-            }
+            if (grp + 1 < g1)
+                load_share(buf, grp + 1, q, 0, ti);
         });
     };
 
@@ -363,7 +384,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     load_scales(sbuf, g0);
     __syncthreads();
 #pragma unroll
-    for (int x = 0; x < 2 * TI; ++x)
+    for (int x = 0; x < TI + TJ; ++x)
         load(buf1, g0, 1, x);
     read_scales(sa, sb);
 #pragma unroll
@@ -388,8 +409,9 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     // time through its part of LDS instead and writes whole lines.
     // (Place c ^ r of row r for its 16-byte column c: no bank conflicts.)
     constexpr int kLanes = 8 * TI, kPer = 64 / kLanes;   // lanes of a row, rows of a store
-    static_assert(4 * 32 * kLanes * 16 <= kRows * 128, "the waves' rows take a code buffer");
-    float4 *mine = reinterpret_cast<float4 *>(buf0) + wave * 32 * kLanes;
+    static_assert(4 * 32 * kLanes * 16 <= kRows * 128 || TJ < TI, "the waves' rows take a code buffer");
+    constexpr bool kApart = 4 * 32 * kLanes * 16 > kRows * 128;   // or both
+    float4 *mine = reinterpret_cast<float4 *>(kApart && wave >= 2 ? buf1 : buf0) + (kApart ? wave % 2 : wave) * 32 * kLanes;
     const int col = n0 + wi * 32 * TI + l % kLanes * 4;
     __syncthreads();
 #pragma unroll
@@ -438,37 +460,40 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(const float *__restrict__ p
     }
 }
 
-// How a product is run: few rows (mx_rows_kernel), or tiles of 64 t x 64 t, k in `parts`.
+// How a product is run: ti = 0: few rows (mx_rows_kernel); else in tiles of 64 ti x 64 tj, k in `parts`.
 struct MxPlan {
-    int t, parts;
+    int ti, tj, parts;
 };
-constexpr int kRowsMost = 64;
+// Up to 8 rows of up to 8192 elements one launch of the row kernel; the tiles, which stream the weights
+// through LDS in whole lines, need a second launch for the sums. Measured, us a call, row kernel and
+// tiles: 1 x 9216 x 5120 9.1 and 10.6, 8 x 9216 x 5120 10.4 and 11.2, 16 x 9216 x 5120 12.3 and 11.0,
+// 1 x 5120 x 17408 16.4 and 15.0, 24 x 5120 x 17408 33 and 16.7.
+constexpr int kRowsMost = 8, kRowsMostK = 8192;
+int64_t tile_count(int m, int n, int ti, int tj) { return (int64_t)((m + 64 * tj - 1) / (64 * tj)) * ((n + 64 * ti - 1) / (64 * ti)); }
 MxPlan plan_gemm(int m, int n, int k)
 {
-    if (m <= kRowsMost)
-        return {0, 1};
-    const int64_t big = (int64_t)((m + 255) / 256) * ((n + 255) / 256);
-    if (big >= 192)
-        return {4, 1};
-    const int64_t small = (int64_t)((m + 127) / 128) * ((n + 127) / 128);
-    const int groups = (k + kGroup - 1) / kGroup;
-    const int parts = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / small), std::max(1, groups / 2));
-    return {2, parts};
+    if (m <= kRowsMost && k <= kRowsMostK)
+        return {0, 0, 1};
+    if (tile_count(m, n, 4, 4) >= 192)
+        return {4, 4, 1};
+    const int tj = m <= 64 ? 1 : 2, groups = (k + kGroup - 1) / kGroup;
+    const int64_t tiles = tile_count(m, n, 2, tj);
+    return {2, tj, (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tiles), std::max(1, groups / 2))};
 }
 
 template <class T>
 int launch_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, T *y, float *part, hipStream_t stream)
 {
     const MxPlan plan = plan_gemm(m, w->n, w->k);
-    if (plan.t) {
-        const int side = 64 * plan.t;
-        const int64_t tiles = (int64_t)((m + side - 1) / side) * ((w->n + side - 1) / side);
-        const dim3 grid((unsigned)((tiles + 7) / 8 * 8), plan.parts);
+    if (plan.ti) {
+        const dim3 grid((unsigned)((tile_count(m, w->n, plan.ti, plan.tj) + 7) / 8 * 8), plan.parts);
         const MxArgs a = {w->codes, w->scales, codes, scales, m, w->n, w->k, y, plan.parts > 1 ? part : nullptr, plan.parts};
-        if (plan.t == 4)
+        if (plan.ti == 4)
             hipLaunchKernelGGL((mx_tile_kernel<4, 4, T>), grid, dim3(256), 0, stream, a);
-        else
+        else if (plan.tj == 2)
             hipLaunchKernelGGL((mx_tile_kernel<2, 2, T>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((mx_tile_kernel<2, 1, T>), grid, dim3(256), 0, stream, a);
         if (hipGetLastError() != hipSuccess)
             return TB_EHIP;
         if (plan.parts > 1) {
@@ -478,24 +503,10 @@ int launch_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, 
         }
         return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
     }
-    const int waves = std::min(kRowWaves, w->k / kBlock);
-    const int mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-    const int per = 65535 * 16 * mt;   // activation rows of one launch (grid.y)
-    for (int r0 = 0; r0 < m; r0 += per) {
-        const int mc = std::min(per, m - r0);
-        const dim3 grid((w->n + 15) / 16, (mc + 16 * mt - 1) / (16 * mt));
-        const uint8_t *ac = codes + (size_t)r0 * (w->k / 2), *as = scales + (size_t)r0 * (w->k / kMxBlock);
-        T *out = y + (size_t)r0 * w->n;
-        if (mt == 1)
-            hipLaunchKernelGGL((mx_rows_kernel<1, T>), grid, dim3(64 * waves), 0, stream, w->codes, w->scales, ac, as, mc, w->n, w->k, out);
-        else if (mt == 2)
-            hipLaunchKernelGGL((mx_rows_kernel<2, T>), grid, dim3(64 * waves), 0, stream, w->codes, w->scales, ac, as, mc, w->n, w->k, out);
-        else
-            hipLaunchKernelGGL((mx_rows_kernel<4, T>), grid, dim3(64 * waves), 0, stream, w->codes, w->scales, ac, as, mc, w->n, w->k, out);
-        if (hipGetLastError() != hipSuccess)
-            return TB_EHIP;
-    }
-    return TB_OK;
+    const int waves = std::min(kRowWaves, (w->k + 255) / 256);
+    hipLaunchKernelGGL((mx_rows_kernel<T>), dim3((w->n + 15) / 16), dim3(64 * waves), 0, stream, w->codes, w->scales, codes, scales, m,
+                       w->n, w->k, y);
+    return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
 template <class T>
