@@ -172,6 +172,10 @@ __device__ __forceinline__ v4i transpose4(uint32_t a, uint32_t b, uint32_t c, ui
                (int)__builtin_amdgcn_perm(cdh, abh, 0x05040100u), (int)__builtin_amdgcn_perm(cdh, abh, 0x07060302u)};
 }
 
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v8i join(v4i a, v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
 template <int FMT>
 struct Core;
 // Ternary: of a block's 8 code words lane group g holds words 2g, 2g + 1; matrix instruction s
@@ -187,6 +191,19 @@ struct Core<TB_FMT_TERNARY2> {
         decode_ternary(s ? w.y : w.x, a, b, c, d);
         return v4i{(int)a, (int)b, (int)c, (int)d};
     }
+    // As 4-bit floats 2 w: word x makes the registers of its even and of its odd weights. A code's
+    // upper bit is the sign, the difference of its bits the 2: 3 is -0. Six operations for 16 weights.
+    __device__ __forceinline__ v8i floats() const
+    {
+        v8i o = {};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t v = x ? w.y : w.x, r = (v & 0xAAAAAAAAu) | ((v ^ (v >> 1)) & 0x55555555u);
+            o[2 * x] = (int)((r << 2) & 0xCCCCCCCCu);
+            o[2 * x + 1] = (int)(r & 0xCCCCCCCCu);
+        }
+        return o;
+    }
 };
 // Sign: lane group g holds word g of a block's 4, the weights 32 g .. 32 g + 31; bit j of its
 // bytes are the weights {j, j+8, j+16, j+24}. Instruction s takes j = 4 s .. 4 s + 3, as +1 / -1.
@@ -201,6 +218,16 @@ struct Core<TB_FMT_SIGN1> {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             o[j] = (int)__builtin_amdgcn_perm(0u, 0x000001FFu, (w >> (4 * s + j)) & 0x01010101u);
+        return o;
+    }
+    // As 4-bit floats -2 w (a set bit, +1, is the sign): register x holds the weights 4 n + x. Seven
+    // operations for 32 weights.
+    __device__ __forceinline__ v8i floats() const
+    {
+        v8i o = {};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            o[x] = (int)(((w << (3 - x)) & 0x88888888u) | 0x44444444u);
         return o;
     }
 };
@@ -257,6 +284,48 @@ __device__ __forceinline__ void stage_piece(uint8_t *lds, int u, int row, int un
         o = s ? transpose4(x, y, v.y, v.w) : transpose4(v.x, v.z, x, y);
     }
     reinterpret_cast<v4i *>(lds)[(u * 8 + s * 4 + g) * T + (row ^ g)] = o;
+}
+
+// For the few-pairs kernel: the activations as the sum of two 8-bit floats (4 exponent bits), a
+// sign and half of the magnitude each: |q| = 16 h + l, and the bytes 0 .. 15 are the floats 0 .. 15 x 2^-9,
+// the numbers below 2^-6 and the binade from there on alike. So one instruction of 128 (its matrices' scales are powers of two) multiplies a block by
+// weights of 4 bits, that cost a third of the operations that bytes cost to make, and its sums are
+// whole numbers below 2^24, exact in float32, that need no conversion. An operand's lane holds the 16-byte
+// chunks c = 0, 1, of lane groups 2 c + g / 2, their registers 2 (g % 2) and 2 (g % 2) + 1: piece s of lane group G
+// goes to plane (c, g) = (G / 2, 2 (G % 2) + s) of the block.
+// Rows 2 NE (t % 4) + 2 (t / 4) and the next hold pair t's lower and upper halves, so that both end in
+// one lane. Row r stands at r ^ 2 g: the pieces that a wave stages spread over the banks.
+// Sign: the weights are the 4-bit floats' negatives, so the activations' signs are turned.
+template <int FMT, int NE>
+__device__ __forceinline__ void stage_split(uint8_t *lds, int u, int t, int unit, uint4 v)
+{
+    uint32_t x[4];
+    int G;
+    if constexpr (FMT == TB_FMT_TERNARY2) {
+        G = (unit & 2) | unit >> 2;   // words 0, 2, 4, 6 are held by lane groups 0, 2, 1, 3 (StepRow)
+        x[0] = __builtin_amdgcn_perm(v.y, v.x, 0x06040200u), x[1] = __builtin_amdgcn_perm(v.w, v.z, 0x06040200u);
+        x[2] = __builtin_amdgcn_perm(v.y, v.x, 0x07050301u), x[3] = __builtin_amdgcn_perm(v.w, v.z, 0x07050301u);
+    } else {
+        // a code word meets two pieces: the even lane makes registers 0 and 1's chunk, the odd one the other
+        G = unit >> 1;
+        const bool odd = unit & 1;
+        const v4i o = transpose4(v.x, v.y, v.z, v.w);
+        const uint32_t p = row_xor((uint32_t)(odd ? o[0] : o[2]), 1), q = row_xor((uint32_t)(odd ? o[1] : o[3]), 1);
+        x[0] = odd ? p : o[0], x[1] = odd ? o[2] : p, x[2] = odd ? q : o[1], x[3] = odd ? o[3] : q;
+    }
+    v4i low, high;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t sign = x[j] & 0x80808080u, ones = sign >> 7, mag = (x[j] ^ ((sign - ones) | sign)) + ones;
+        const uint32_t top = FMT == TB_FMT_SIGN1 ? sign ^ 0x80808080u : sign;
+        low[j] = (int)((mag & 0x0F0F0F0Fu) | top);
+        high[j] = (int)(((mag >> 4) & 0x0F0F0F0Fu) | top);
+    }
+    const int c = G >> 1, g = 2 * (G & 1) + (unit & 1);
+    const int row = 2 * NE * (t & 3) + 2 * (t >> 2);
+    v4i *plane = reinterpret_cast<v4i *>(lds) + (u * 8 + c * 4 + g) * (8 * NE);
+    plane[row ^ (2 * g)] = low;
+    plane[(row + 1) ^ (2 * g)] = high;
 }
 
 // A row of a tile's pair t
@@ -621,18 +690,19 @@ __global__ __launch_bounds__(1024) void moe_wide_kernel(MoeArgs a, uint32_t firs
 }
 
 // ------------------------------------------------------------------------------------
-// Few pairs per expert: 16 pairs, 4 waves of 32 weight rows, so that the experts' rows spread over
-// the chip; the weights' way from memory bounds it. Steps are loaded one ahead, and up to 32 blocks of
-// the activations there are are staged at a time.
+// Few pairs per expert: tiles of 8 pairs, 8 waves of 16 weight rows. Here the operations that make
+// operands of the codes count most, for they serve 8 pairs at most, so the product is of 4-bit by 8-bit floats (stage_split): at
+// 5 pairs of each of 16 experts, sign, 2 x 2176 x 5120, 40 us with bytes and tiles of 16 pairs of 4 waves, 27 us here. The
+// codes are loaded a step ahead. What bounds it: each unit of 16 rows by a block takes some 22 vector operations
+// and 2 KB read from LDS, and few workgroups leave the loads' and the staging's latency bare.
 // ------------------------------------------------------------------------------------
 template <int FMT, bool TWO>
 struct NarrowShape {
-    static constexpr int kWaves = 4, kThreads = 64 * kWaves;
-    static constexpr int kT = 16;
-    static constexpr int kCols = TWO ? 16 * kWaves : 32 * kWaves;
+    static constexpr int kWaves = 8, kThreads = 64 * kWaves;
+    static constexpr int kT = 8;
+    static constexpr int kCols = TWO ? 8 * kWaves : 16 * kWaves;   // gate/up: the upper waves take up's rows
     static constexpr int kPhases = Core<FMT>::kStep / 4;
-    static constexpr int kBlocks = 32;                        // staged at a time
-    static constexpr int kActBytes = kBlocks * 8 * kT * 16, kDqBytes = kBlocks * kT * 4;
+    static constexpr int kActBytes = 64 * 1024, kDqBytes = 1024;
     static constexpr int kLds = kActBytes + kDqBytes;
 };
 
@@ -642,98 +712,123 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
 {
     using C = Core<FMT>;
     using S = NarrowShape<FMT, TWO>;
-    constexpr int R = 2;   // row tiles of a wave (gate/up: the same rows of both)
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, i = l & 15, g = l >> 4;
     const int nb = a.k / kBlock, steps = (nb + C::kStep - 1) / C::kStep;
 
-    WeightRows<FMT> rows[R] = {{a, 0, tile.expert, n0 + 16 * (TWO ? wave : 2 * wave) + i, nb},
-                                     {a, TWO ? 1 : 0, tile.expert, n0 + 16 * (TWO ? wave : 2 * wave + 1) + i, nb}};
-    StepRow<FMT> w[2][R];
-    auto load_weights = [&](int j, int step) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            w[j][r].load(rows[r].codes, rows[r].scales, rows[r].coff + g * 16, rows[r].soff & ~3u, nb, step);
-    };
+    constexpr int T = 4 * NE, kBlocks = 64 / NE;   // pairs of a tile, blocks staged at a time
+    constexpr int kBlockPieces = 8 * 2 * T;        // 16-byte pieces of a block: 8 planes of 2 T rows
+    static_assert(kBlocks * kBlockPieces * 16 == S::kActBytes && kBlocks * T * 4 == S::kDqBytes, "");
+    float *dq_s = reinterpret_cast<float *>(lds + S::kActBytes);
+    const int act_scale = 127 + 9 + 4 * (i & 1);   // of A row i, lower or upper halves: 2^9 or 2^13
+
+    const int m = TWO && wave >= S::kWaves / 2, col = n0 + 16 * (TWO ? wave % (S::kWaves / 2) : wave) + i;
+    const WeightRows<FMT> rows(a, m, tile.expert, col, nb);
+    StepRow<FMT> w[2];
+    auto load_weights = [&](int j, int step) { w[j].load(rows.codes, rows.scales, rows.coff + g * 16, rows.soff & ~3u, nb, step); };
+    const int my_row = (int)act_row<TWO>(a, tile.slot + min(l & 7, tile.rows - 1));   // of pair l % 8
     load_weights(0, 0);
 
-    // staging: 8 blocks of a pair by a wave, 32 by the workgroup
+    // Staging: the pieces of all pairs are dealt to the threads, all loads in flight at once.
     auto stage = [&](int c0) {
-        const int u = tid >> 3, at = min(c0 + u, nb - 1);
-#pragma unroll 4
-        for (int tok = 0; tok < tile.rows; ++tok) {
-            const size_t row = act_row<TWO>(a, tile.slot + tok);
-            const uint4 v = *reinterpret_cast<const uint4 *>(a.q + row * a.k + at * kBlock + (tid & 7) * 16);
-            stage_piece<FMT, S::kT>(lds, u, pair_row(tok), tid & 7, v);
-            if (tid < S::kBlocks)
-                reinterpret_cast<float *>(lds + S::kActBytes)[tid * S::kT + pair_row(tok)] = c0 + tid < nb ? a.dq[row * nb + c0 + tid] : 0.0f;
+        constexpr int kLoads = T * kBlocks * 8 / S::kThreads, kDq = (T * kBlocks + S::kThreads - 1) / S::kThreads;
+        // whole steps: blocks past the end read the last one (what is left in LDS may be NaN), with dq 0
+        const int blocks = min(kBlocks, nb - c0), padded = (blocks + C::kStep - 1) / C::kStep * C::kStep;
+        const int items = tile.rows * padded;
+        // x / padded for x < 512: x + 1/2 over it is farther from a whole number than the product's rounding
+        const float inv = 1.0f / (float)padded;
+        auto split = [&](int x, int &tok, int &u) {
+            tok = (int)(((float)x + 0.5f) * inv);
+            u = x - tok * padded;
+        };
+        float dv[kDq];
+        uint4 v[kLoads];
+        int tok, u;
+#pragma unroll
+        for (int j = 0; j < kDq; ++j) {
+            split(tid + j * S::kThreads, tok, u);
+            const int row = __shfl(my_row, tok & 7);
+            dv[j] = 0.0f;
+            if (tid + j * S::kThreads < items && u < blocks)
+                dv[j] = a.dq[(size_t)row * nb + c0 + u];
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (j * (S::kThreads / 8) < items) {   // the same for all lanes
+                split(min(j * (S::kThreads / 8) + (tid >> 3), items - 1), tok, u);
+                const int row = __shfl(my_row, tok);
+                v[j] = *reinterpret_cast<const uint4 *>(a.q + (size_t)row * a.k + (c0 + min(u, blocks - 1)) * kBlock + (tid & 7) * 16);
+            }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (j * (S::kThreads / 8) < items) {
+                split(min(j * (S::kThreads / 8) + (tid >> 3), items - 1), tok, u);
+                stage_split<FMT, NE>(lds, u, tok, tid & 7, v[j]);
+            }
+#pragma unroll
+        for (int j = 0; j < kDq; ++j) {
+            split(tid + j * S::kThreads, tok, u);
+            if (tid + j * S::kThreads < items)
+                dq_s[u * T + NE * (tok & 3) + (tok >> 2)] = dv[j];
         }
     };
+    stage(0);
     if (steps > 1)
         load_weights(1, 1);
-    stage(0);
     __syncthreads();
 
-    float acc[R][NE];
+    float acc[NE];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-            acc[r][e] = 0.0f;
+    for (int e = 0; e < NE; ++e)
+        acc[e] = 0.0f;
     for (int s0 = 0; s0 < steps; s0 += 2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int step = s0 + j;
             if (step < steps) {   // the same for all waves
-                constexpr int kPer = S::kBlocks / C::kStep;   // steps staged at a time
+                constexpr int kPer = kBlocks / C::kStep;   // steps staged at a time
                 if (step && step % kPer == 0) {
                     __syncthreads();
                     stage(step * C::kStep);
                     __syncthreads();
                 }
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    w[j][r].deal(rows[r].soff & 2);
-                const int u0 = step % kPer * C::kStep;
-                const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kT + (i ^ g);
-                const float *d = reinterpret_cast<const float *>(lds + S::kActBytes) + u0 * S::kT + 4 * g;
-                float part0[R][NE], part1[R][NE];
+                w[j].deal(rows.soff & 2);
+                const int u0 = step % kPer * C::kStep, left = nb - step * C::kStep;
+                const v4i *act = reinterpret_cast<const v4i *>(lds) + u0 * kBlockPieces + g * (2 * T) +
+                                 ((NE == 1 ? 2 * (i >> 2) + (i & 1) : i) ^ (2 * g));
+                const float *d = dq_s + u0 * T + NE * g;
+                float part0[NE], part1[NE];
 #pragma unroll
                 for (int q = 0; q < S::kPhases; ++q) {
-                    float sum[R][NE];
+                    float sum[NE] = {};
+                    if (q == 0 || C::kStep - 4 * q - 3 < left) {   // else all of its blocks are past the end
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float term[R][2][NE];
+                        for (int h = 0; h < 2; ++h) {
+                            float term[2][NE];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int x = 4 * q + 2 * h + b, blk = x ? C::kStep - x : 0;
-                            const v4i a0 = act[blk * 8 * S::kT], a1 = act[(blk * 8 + 4) * S::kT];
-#pragma unroll
-                            for (int r = 0; r < R; ++r) {
-                                const C core = w[j][r].block(blk);
-                                v4i z = {0, 0, 0, 0};
-                                z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, core.weights(0), z, 0, 0, 0);
-                                z = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, core.weights(1), z, 0, 0, 0);
-                                const float s = w[j][r].scale(blk);
+                            for (int b = 0; b < 2; ++b) {
+                                const int x = 4 * q + 2 * h + b, blk = x ? C::kStep - x : 0;
+                                const v4i *p = act + blk * kBlockPieces;
+                                // the weights' scale takes back their 2, the activations' makes whole numbers of
+                                // their lower and upper halves
+                                const v4f z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    join(p[0], p[4 * 2 * T]), w[j].block(blk).floats(), v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 4, 0, act_scale, 0, 126);
+                                const float s = w[j].scale(blk);
 #pragma unroll
                                 for (int e = 0; e < NE; ++e)
-                                    term[r][b][e] = (s * d[blk * S::kT + e]) * (float)z[e];
+                                    term[b][e] = (s * d[blk * T + e]) * (z[2 * e] + z[2 * e + 1]);
                             }
-                        }
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
 #pragma unroll
                             for (int e = 0; e < NE; ++e) {
-                                const float v = term[r][0][e] + term[r][1][e];
-                                sum[r][e] = h ? sum[r][e] + v : v;
+                                const float v = term[0][e] + term[1][e];
+                                sum[e] = h ? sum[e] + v : v;
                             }
+                        }
                     }
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int e = 0; e < NE; ++e) {
-                            add_phase<S::kPhases>(q, sum[r][e], part0[r][e], part1[r][e], acc[r][e]);
-                            asm volatile("" : "+v"(sum[r][e]));
-                        }
+                    for (int e = 0; e < NE; ++e) {
+                        add_phase<S::kPhases>(q, sum[e], part0[e], part1[e], acc[e]);
+                        asm volatile("" : "+v"(sum[e]));
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (step + 2 < steps)
@@ -741,18 +836,29 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
             }
         }
     }
+    if constexpr (TWO) {   // u through LDS to the lanes that hold its g
+        float *u = reinterpret_cast<float *>(lds) + (wave % (S::kWaves / 2)) * (64 * NE) + l;
+        __syncthreads();
+        if (m)
+#pragma unroll
+            for (int e = 0; e < NE; ++e)
+                u[64 * e] = acc[e];
+        __syncthreads();
+        if (m)
+            return;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            acc[e] = silu_gate(acc[e], u[64 * e]);
+    }
 #pragma unroll
     for (int e = 0; e < NE; ++e)
-        if (float *o = pair_out<TWO>(a, tile, g + 4 * e)) {
-            if (rows[0].col < a.n)
-                o[rows[0].col] = TWO ? silu_gate(acc[0][e], acc[1][e]) : acc[0][e];
-            if (!TWO && rows[1].col < a.n)
-                o[rows[1].col] = acc[1][e];
-        }
+        if (float *o = pair_out<TWO>(a, tile, g + 4 * e))
+            if (col < a.n)
+                o[col] = acc[e];
 }
 
 template <int FMT, bool TWO>
-__global__ __launch_bounds__(256) void moe_narrow_kernel(MoeArgs a, uint32_t first)
+__global__ __launch_bounds__(512, 4) void moe_narrow_kernel(MoeArgs a, uint32_t first)
 {
     using S = NarrowShape<FMT, TWO>;
     __shared__ __align__(16) uint8_t lds[S::kLds];
@@ -763,10 +869,8 @@ __global__ __launch_bounds__(256) void moe_narrow_kernel(MoeArgs a, uint32_t fir
     const int n0 = block * S::kCols;
     if (tile.rows <= 4)
         narrow_product<FMT, TWO, 1>(a, tile, n0, lds);
-    else if (tile.rows <= 8)
-        narrow_product<FMT, TWO, 2>(a, tile, n0, lds);
     else
-        narrow_product<FMT, TWO, 4>(a, tile, n0, lds);
+        narrow_product<FMT, TWO, 2>(a, tile, n0, lds);
 }
 
 // rotquant of the slots in use: rows [0, offsets[experts]) of h. One 128-block per 16 lanes.
