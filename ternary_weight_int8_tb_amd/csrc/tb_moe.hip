@@ -987,8 +987,8 @@ int launch_items(int64_t tiles, int parts, F &&launch)
 // Tiles of `rows` pairs at most: every expert's last may be partly filled, and none is empty.
 int64_t most_tiles(const MoeArgs &a, int rows) { return std::min<int64_t>(a.pairs, (int64_t)a.pairs / rows + a.experts); }
 
-// Wide tiles from an average of 16 pairs per expert on.
-bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)experts * 16; }
+// Wide tiles from an average of 24 pairs per expert on.
+bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)experts * 24; }
 
 template <int FMT, bool TWO>
 int launch_product_as(const MoeArgs &a, hipStream_t stream)
