@@ -10,7 +10,7 @@
 // the whole row, goes into dq alone: q is final as soon as its block has been read, and the row
 // is read once. It also makes q independent of how the row's squares are summed.
 //
-// Bound: memory. One workgroup per row; 16 lanes hold a 128-block, 8 elements each, and all
+// Bound: memory. A workgroup holds a whole row; 16 lanes hold a 128-block, 8 elements each, and all
 // exchanges are DPP. Squares are summed in fp32 over a lane's 8 elements and in fp64 from there,
 // so neither the row's length nor the order of its waves shows in the fp32 result.
 #include <hip/hip_runtime.h>
@@ -48,8 +48,120 @@ __device__ __forceinline__ void add_rows(const Eight<T> &x, const Eight<T> &res,
     }
 }
 
+// The lane's 8 of u * r's codes, the sign of rotate_signed taken back; amax: the block's.
+__device__ __forceinline__ uint2 codes(const float (&u)[8], float amax, float sign)
+{
+    uint32_t w[2] = {0u, 0u};
+    if (amax >= kZeroBlock) {
+        const float inv = (127.0f / amax) * sign;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // |u * inv| <= 127 (1 + 2^-23); adding 1.5 * 2^23 rounds it to an integer, ties
+            // to even, whose low byte is the code
+            const uint32_t c = __float_as_uint(u[e] * inv + 12582912.0f) & 0xffu;
+            w[e >> 2] |= c << (8 * (e & 3));
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// The sum over a wave's lanes, in every lane.
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const uint64_t b = (uint64_t)__double_as_longlong(v);
+        v += __longlong_as_double((long long)((uint64_t)partner((uint32_t)(b >> 32), s) << 32 | partner((uint32_t)b, s)));
+    }
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// r of a row from its waves' sums.
+__device__ __forceinline__ float norm_of(const double *part, int waves, int k, float eps)
+{
+    double total = 0.0;
+    for (int w = 0; w < waves; ++w)
+        total += part[w];
+    const double mean = total / (double)k + (double)eps;
+    return mean > 0.0 ? (float)(1.0 / sqrt(mean)) : 0.0f;   // a row of zeros, eps = 0
+}
+
+// Rows of up to 64 blocks: a lane's 8 elements of a row stay in registers until y, those of gamma for
+// all rows of the workgroup, and the next row's are on their way while this one's norm is
+// summed (8192 rows of 5120 bf16 with res: 85 us with a row per workgroup, which waits for its loads and
+// then for its sum; 55 us so).
+// LDS is used in turn by odd and even rows, so that one barrier per row is enough.
 template <class T>
 __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
+    const T *x, const T *res, const float *__restrict__ gamma, int m, int nb, float eps, float unit, T *res_out, T *y,
+    int8_t *__restrict__ q, float *__restrict__ dq)
+{
+    __shared__ float amax_s[2][kMaxThreads / 16];
+    __shared__ double part_s[2][kMaxThreads / 64];
+    const int tid = threadIdx.x, lane16 = tid & 15, b = tid >> 4, waves = blockDim.x >> 6;
+    const bool on = b < nb;   // else the group holds no block: it computes with zeros
+    const float sign = chunk_sign(lane16);
+    const int at = min(b, nb - 1) * kBlock + chunk_of(lane16) * 8;
+    float g[8];
+    {
+        Eight<float> eg;
+        eg.load(gamma + at);
+        eg.get(g);
+    }
+    Eight<T> ex, er;
+    auto load = [&](size_t row) {
+        const size_t i = row * (size_t)nb * kBlock + at;
+        ex.load(x + i);
+        if (res)
+            er.load(res + i);
+    };
+    load(blockIdx.x);
+    int turn = 0;
+    for (size_t row = blockIdx.x; row < (size_t)m; row += gridDim.x, turn ^= 1) {
+        const size_t i = row * (size_t)nb * kBlock + at;
+        Eight<T> es;
+        float v[8], u[8];
+        add_rows(ex, er, res != nullptr, es, v);
+        if (row + gridDim.x < (size_t)m)
+            load(row + gridDim.x);
+        if (res_out && on)
+            es.store(res_out + i);
+        float sq = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sq = fmaf(v[e], v[e], sq);
+            u[e] = v[e] * g[e];
+        }
+        const double sum = wave_sum(on ? (double)sq : 0.0);
+        if ((tid & 63) == 0)
+            part_s[turn][tid >> 6] = sum;
+        rotate_signed(u, lane16);
+        const float amax = __uint_as_float(amax_bits<4>(u));
+        const uint2 c = codes(u, amax, sign);
+        if (on)
+            *reinterpret_cast<uint2 *>(q + i) = c;
+        if (lane16 == 0)
+            amax_s[turn][b] = amax >= kZeroBlock ? amax : 0.0f;
+        __syncthreads();
+        if (tid >= 64 && !y)
+            continue;
+        const float r = norm_of(part_s[turn], waves, nb * kBlock, eps);
+        if (tid < nb)   // the first wave's lanes
+            dq[row * nb + tid] = amax_s[turn][tid] != 0.0f ? amax_s[turn][tid] * (r * unit) : 0.0f;
+        if (y && on) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = (v[e] * r) * g[e];
+            es.set(v);
+            es.store(y + i);
+        }
+    }
+}
+
+// Longer rows: a row per workgroup, in passes of 64 blocks; for y it is read again.
+template <class T>
+__global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
     const T *x, const T *res, const float *__restrict__ gamma, int m, int nb, float eps, float unit, T *res_out, T *y,
     int8_t *__restrict__ q, float *__restrict__ dq)
 {
@@ -60,79 +172,62 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
     const int at = chunk_of(lane16) * 8;
 
     for (size_t row = blockIdx.x; row < (size_t)m; row += gridDim.x) {
-    const size_t base = row * (size_t)nb * kBlock;
-    double sum = 0.0;
-    for (int b = tid >> 4; b < nb; b += groups) {
-        const size_t i = base + (size_t)b * kBlock + at;
-        Eight<T> ex, er, es;
-        Eight<float> eg;
-        ex.load(x + i);
-        if (res)
-            er.load(res + i);
-        eg.load(gamma + b * kBlock + at);
-        float v[8], g[8];
-        add_rows(ex, er, res != nullptr, es, v);
-        if (res_out)
-            es.store(res_out + i);
-        eg.get(g);
-        float sq = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sq = fmaf(v[e], v[e], sq);
-            v[e] *= g[e];
-        }
-        sum += (double)sq;
-        rotate_signed(v, lane16);
-        const float amax = __uint_as_float(amax_bits<4>(v));
-        uint32_t w[2] = {0u, 0u};
-        if (amax >= kZeroBlock) {
-            const float inv = (127.0f / amax) * sign;
+        const size_t base = row * (size_t)nb * kBlock;
+        double sum = 0.0;
+        for (int b = tid >> 4; b < nb; b += groups) {
+            const size_t i = base + (size_t)b * kBlock + at;
+            Eight<T> ex, er, es;
+            Eight<float> eg;
+            ex.load(x + i);
+            if (res)
+                er.load(res + i);
+            eg.load(gamma + b * kBlock + at);
+            float v[8], g[8];
+            add_rows(ex, er, res != nullptr, es, v);
+            if (res_out)
+                es.store(res_out + i);
+            eg.get(g);
+            float sq = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // |v * inv| <= 127 (1 + 2^-23); adding 1.5 * 2^23 rounds it to an integer, ties
-                // to even, whose low byte is the code
-                const uint32_t c = __float_as_uint(v[e] * inv + 12582912.0f) & 0xffu;
-                w[e >> 2] |= c << (8 * (e & 3));
+                sq = fmaf(v[e], v[e], sq);
+                v[e] *= g[e];
             }
+            sum += (double)sq;
+            rotate_signed(v, lane16);
+            const float amax = __uint_as_float(amax_bits<4>(v));
+            *reinterpret_cast<uint2 *>(q + i) = codes(v, amax, sign);
+            if (lane16 == 0)
+                amax_s[b] = amax >= kZeroBlock ? amax : 0.0f;
         }
-        *reinterpret_cast<uint2 *>(q + i) = make_uint2(w[0], w[1]);
-        if (lane16 == 0)
-            amax_s[b] = amax >= kZeroBlock ? amax : 0.0f;
-    }
-    for (int off = 32; off; off >>= 1)
-        sum += __shfl_xor(sum, off);
-    if ((tid & 63) == 0)
-        part_s[tid >> 6] = sum;
-    __syncthreads();
-    double total = 0.0;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w)
-        total += part_s[w];
-    const double mean = total / ((double)nb * kBlock) + (double)eps;
-    const float r = mean > 0.0 ? (float)(1.0 / sqrt(mean)) : 0.0f;   // a row of zeros, eps = 0
-    const float step = r * unit;
-    for (int b = tid; b < nb; b += blockDim.x)
-        dq[row * nb + b] = amax_s[b] != 0.0f ? amax_s[b] * step : 0.0f;
+        sum = wave_sum(sum);
+        if ((tid & 63) == 0)
+            part_s[tid >> 6] = sum;
+        __syncthreads();
+        const float r = norm_of(part_s, blockDim.x >> 6, nb * kBlock, eps);
+        for (int b = tid; b < nb; b += blockDim.x)
+            dq[row * nb + b] = amax_s[b] != 0.0f ? amax_s[b] * (r * unit) : 0.0f;
 
-    if (y)
-    for (int b = tid >> 4; b < nb; b += groups) {
-        const size_t i = base + (size_t)b * kBlock + at;
-        Eight<T> ex, er, es;
-        Eight<float> eg;
-        float v[8], g[8];
-        // res_out may be x or res itself: what this lane stored there is s
-        ex.load(res_out ? res_out + i : x + i);
-        if (res && !res_out)
-            er.load(res + i);
-        eg.load(gamma + b * kBlock + at);
-        add_rows(ex, er, res && !res_out, es, v);
-        eg.get(g);
+        if (y)
+            for (int b = tid >> 4; b < nb; b += groups) {
+                const size_t i = base + (size_t)b * kBlock + at;
+                Eight<T> ex, er, es;
+                Eight<float> eg;
+                float v[8], g[8];
+                // res_out may be x or res itself: what this lane stored there is s
+                ex.load(res_out ? res_out + i : x + i);
+                if (res && !res_out)
+                    er.load(res + i);
+                eg.load(gamma + b * kBlock + at);
+                add_rows(ex, er, res && !res_out, es, v);
+                eg.get(g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = (v[e] * r) * g[e];
-        es.set(v);
-        es.store(y + i);
-    }
-    __syncthreads();   // the next row's maxima and sums take this one's place
+                for (int e = 0; e < 8; ++e)
+                    v[e] = (v[e] * r) * g[e];
+                es.set(v);
+                es.store(y + i);
+            }
+        __syncthreads();   // the next row's maxima and sums take this one's place
     }
 }
 
@@ -141,12 +236,20 @@ int launch(const void *x, const void *res, const float *gamma, int m, int k, flo
            int8_t *q, float *dq, hipStream_t stream)
 {
     const int nb = k / kBlock;
-    // the row's blocks in as few equal passes as 1024 threads allow
-    const int passes = (nb + kMaxThreads / 16 - 1) / (kMaxThreads / 16);
-    const int waves = ((nb + passes - 1) / passes + 3) / 4;
-    hipLaunchKernelGGL(add_rmsnorm_quant_kernel<T>, dim3(std::min(m, kMaxGrid)), dim3(64 * waves), (size_t)nb * 4, stream,
-                       static_cast<const T *>(x), static_cast<const T *>(res), gamma, m, nb, eps, tbh::dq_unit(),
-                       static_cast<T *>(res_out), static_cast<T *>(y), q, dq);
+    const T *xs = static_cast<const T *>(x), *rs = static_cast<const T *>(res);
+    T *ro = static_cast<T *>(res_out), *ys = static_cast<T *>(y);
+    if (nb <= kMaxThreads / 16) {
+        // as many workgroups as the chip holds: 256 CUs of 32 waves
+        const int waves = (nb + 3) / 4;
+        hipLaunchKernelGGL(add_rmsnorm_quant_kernel<T>, dim3(std::min(m, 256 * (32 / waves))), dim3(64 * waves), 0, stream,
+                           xs, rs, gamma, m, nb, eps, tbh::dq_unit(), ro, ys, q, dq);
+    } else {
+        // the row's blocks in as few equal passes as 1024 threads allow
+        const int passes = (nb + kMaxThreads / 16 - 1) / (kMaxThreads / 16);
+        const int waves = ((nb + passes - 1) / passes + 3) / 4;
+        hipLaunchKernelGGL(add_rmsnorm_quant_long_kernel<T>, dim3(std::min(m, kMaxGrid)), dim3(64 * waves), (size_t)nb * 4,
+                           stream, xs, rs, gamma, m, nb, eps, tbh::dq_unit(), ro, ys, q, dq);
+    }
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
