@@ -12,6 +12,7 @@ without a GPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -355,6 +356,14 @@ def tb_ffn_layers(layers: FfnLayers, x, ws, y, chain: bool = False, stream=None)
 # ---- row operators, microscaled 4-bit products, experts ----------------------------------
 # These check their tensors here (type, shape, contiguity, device) and run on the tensors'
 # device, on its current stream unless one is given.
+# A call costs the host about as much as a launch does, so that they look torch up once and ask for
+# the current device once.
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
+
+
 def _bad(fn: str, why: str):
     raise TbError(fn, TB_EINVAL, why)
 
@@ -374,8 +383,9 @@ def _dtype(fn: str, t) -> int:
 
 def _check(fn: str, device, *arrays) -> None:
     """Each of arrays is (name, tensor, dtype, shape): contiguous, on `device`."""
+    index = device.index
     for name, t, dtype, shape in arrays:
-        if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
             _bad(fn, f"{name} has to be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -386,12 +396,15 @@ def _matrix_rows(fn: str, name: str, t):
 
 
 def _launch(fn: str, device, stream, *args) -> None:
-    import torch
-    if device.index == torch.cuda.current_device():
-        _call(fn, *args, _stream(stream))
-    else:
+    torch = _torch()
+    index = torch._C._cuda_getDevice()   # the tensors are there, so the device is initialised
+    if device.index != index:
         with torch.cuda.device(device):
             _call(fn, *args, _stream(stream))
+    elif stream is None:
+        _call(fn, *args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        _call(fn, *args, _stream(stream))
 
 
 def _ptr(t):
@@ -403,7 +416,7 @@ def tb_add_rmsnorm_quant_i8(x, res, gamma, eps: float, res_out, y, q, dq, stream
 
     x, res (or None) [m][k] of one type (float32, bfloat16, float16); gamma float32 [k]. res_out
     (or None; may be x or res) takes s, y (or None) the normed rows, both in that type."""
-    import torch
+    torch = _torch()
     fn = "tb_add_rmsnorm_quant_i8"
     m, k = _matrix_rows(fn, "x", x)
     dev, dt = x.device, x.dtype
@@ -442,7 +455,7 @@ class Mxfp4:
 
 def tb_mxfp4_quant(x, codes, scales, rotate: bool = False, stream=None) -> None:
     """codes uint8 [m][k/2], scales uint8 [m][k/32] of the rows x [m][k] (rotated first, if asked)."""
-    import torch
+    torch = _torch()
     fn = "tb_mxfp4_quant"
     m, k = _matrix_rows(fn, "x", x)
     code = _dtype(fn, x)
@@ -452,7 +465,7 @@ def tb_mxfp4_quant(x, codes, scales, rotate: bool = False, stream=None) -> None:
 
 def tb_mxfp4_dequant(codes, scales, y, stream=None) -> None:
     """y [m][k] (float32, bfloat16 or float16) = the values that the codes stand for."""
-    import torch
+    torch = _torch()
     fn = "tb_mxfp4_dequant"
     m, k = _matrix_rows(fn, "y", y)
     code = _dtype(fn, y)
@@ -469,7 +482,7 @@ def tb_mxfp4_gemm(w: Mxfp4, codes, scales, y, ws=None, stream=None) -> None:
     """y [m][w.n] (float32, bfloat16 or float16) = the rows (codes, scales) times w's rows.
 
     ws: a uint8 workspace of tb_mxfp4_gemm_workspace_bytes(w, m) bytes, or None where that is 0."""
-    import torch
+    torch = _torch()
     fn = "tb_mxfp4_gemm"
     m, n = _matrix_rows(fn, "y", y)
     code, dev = _dtype(fn, y), y.device
@@ -515,7 +528,7 @@ class Experts:
 def tb_moe_plan(ids, experts: int, offsets, order, stream=None) -> None:
     """Sort the pairs of ids int32 [tokens][topk] by expert: offsets int32 [experts + 1], order
     int32 [tokens * topk]. An id outside [0, experts) belongs to no expert."""
-    import torch
+    torch = _torch()
     fn = "tb_moe_plan"
     t, topk = _matrix_rows(fn, "ids", ids)
     _check(fn, ids.device, ("ids", ids, torch.int32, (t, topk)), ("offsets", offsets, torch.int32, (experts + 1,)),
@@ -528,7 +541,7 @@ def tb_moe_gateup_silu(wg: Experts, wu: Experts, q, dq, topk: int, offsets, orde
 
     q int8 [tokens][k], dq float32 [tokens][k/128]; h float32 [tokens * topk][n] is workspace; qh int8
     [tokens * topk][n], dqh float32 [tokens * topk][n/128]."""
-    import torch
+    torch = _torch()
     fn = "tb_moe_gateup_silu"
     t, k = _matrix_rows(fn, "q", q)
     n, dev, p = wg.n, q.device, t * topk
@@ -543,7 +556,7 @@ def tb_moe_gateup_silu(wg: Experts, wu: Experts, q, dq, topk: int, offsets, orde
 
 def tb_moe_down(wd: Experts, qh, dqh, offsets, order, y, stream=None) -> None:
     """y float32 [tokens * topk][n] = down product of the plan's slots, a row per pair."""
-    import torch
+    torch = _torch()
     fn = "tb_moe_down"
     p, k = _matrix_rows(fn, "qh", qh)
     dev = qh.device
@@ -558,7 +571,7 @@ def tb_moe_down(wd: Experts, qh, dqh, offsets, order, y, stream=None) -> None:
 
 def tb_moe_combine(y, weights, ids, experts: int, out, stream=None) -> None:
     """out [tokens][n] (float32, bfloat16 or float16) = each token's pairs, weighted and summed."""
-    import torch
+    torch = _torch()
     fn = "tb_moe_combine"
     t, topk = _matrix_rows(fn, "ids", ids)
     code, n, dev = _dtype(fn, out), int(out.shape[-1]), ids.device
