@@ -157,9 +157,11 @@ struct Tiles {
             read(offsets, experts, pairs, e0);
         }
         // wave-uniform values, in scalar registers
-        const int src = __ffsll((unsigned long long)__ballot(before + upto > t)) - 1;
+        const int src = max(__ffsll((unsigned long long)__ballot(before + upto > t)) - 1, 0);
         const int r0 = (t - before - __builtin_amdgcn_readlane(upto - tiles, src)) * ROWS;
-        return {e0 + src, __builtin_amdgcn_readlane(lo, src) + r0, min(ROWS, __builtin_amdgcn_readlane(count, src) - r0)};
+        // cut once more: where offsets are no plan's, the numbers of tiles may not fit 32 bits
+        const int slot = min(max(__builtin_amdgcn_readlane(lo, src) + r0, 0), pairs - 1);
+        return {min(e0 + src, experts - 1), slot, min(max(min(ROWS, __builtin_amdgcn_readlane(count, src) - r0), 1), pairs - slot)};
     }
 };
 
@@ -439,12 +441,16 @@ struct StepRow {
         scales[kScaleWords] = buffer_load_u32(s, so + kScaleWords * 4);
     }
     // After the loads, by lane swaps: each block's codes, 16 bytes of which one lane group loaded, in all groups, scales from bit 0 of scales[0] on.
-    // odd: the row's first scale is the upper half of its word
-    __device__ __forceinline__ void deal(bool odd)
+    // odd: the row's first scale is the upper half of its word; left: the blocks from this step's first on
+    __device__ __forceinline__ void deal(bool odd, int left)
     {
 #pragma unroll
         for (int x = 0; x < kScaleWords; ++x)
             scales[x] = __builtin_amdgcn_alignbit(scales[x + 1], scales[x], odd ? 16 : 0);
+        if (left < Core<FMT>::kStep)   // what follows are the next row's: 0 times an infinity is no 0
+#pragma unroll
+            for (int x = 0; x < kScaleWords; ++x)
+                scales[x] &= 2 * x + 1 < left ? 0xffffffffu : 2 * x < left ? 0xffffu : 0u;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             swap32(codes[x].x, codes[x].z);
@@ -569,7 +575,7 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
             }
             const v4i *act = reinterpret_cast<const v4i *>(lds) + (u0 * 8 + g) * S::kT + (i ^ g);
             const float *d = dq_s + u0 * S::kT + 4 * g;
-            w.deal(rows.soff & 2);
+            w.deal(rows.soff & 2, nb - step * C::kStep);
 #pragma unroll
             for (int j = 0; j < S::kPhases; ++j) {
                 float sum[NT][4];
@@ -791,8 +797,8 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
                     stage(step * C::kStep);
                     __syncthreads();
                 }
-                w[j].deal(rows.soff & 2);
                 const int u0 = step % kPer * C::kStep, left = nb - step * C::kStep;
+                w[j].deal(rows.soff & 2, left);
                 const v4i *act = reinterpret_cast<const v4i *>(lds) + u0 * kBlockPieces + g * (2 * T) +
                                  ((NE == 1 ? 2 * (i >> 2) + (i & 1) : i) ^ (2 * g));
                 const float *d = dq_s + u0 * T + NE * g;

@@ -268,6 +268,78 @@ def test_norm_route_experts():
     assert np.linalg.norm(got - want) < 0.03 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("t", [7, 90])   # tiles of few and of many pairs
+def test_every_int8_value(fmt, t):
+    """Rows that no quantiser made: all 256 values of a byte."""
+    layer = layer_of(fmt, 3, 640, 384)
+    rng = np.random.default_rng(83)
+    q = rng.integers(-128, 128, (t, 640)).astype(np.int8)
+    q[0, :256] = np.arange(-128, 128)
+    q[-1] = -128
+    dq = rng.standard_normal((t, 5)).astype(np.float32)
+    dq[t // 2] = 0.0
+    ids = ids_of("any", t, 2, 3, 84)
+    check(Run(layer, q, dq, ids).launch(), ids)
+
+
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("t", [7, 90])
+@pytest.mark.parametrize("k", [640, 1152])   # 5 and 9 blocks: the last step is not full
+def test_scales_that_are_not_finite_stay_in_their_row(fmt, t, k):
+    host = [synth.ffn_layer(85, e, fmt, hidden=256, inter=k).down for e in range(3)]
+    ids = ids_of("any", t, 2, 3, 86)
+    offsets, order = plan_of(ids, 3)
+    qh, dqh = rows(2 * t, k, 87)
+    out = []
+    for plant in (False, True):
+        w = tb.Experts.upload(host)
+        if plant:
+            bits = w.scales.view(torch.float16)
+            bits[:, 0, 0] = float("inf")    # behind the last row of the expert before
+            bits[:, 7, 0] = float("-inf")
+            bits[:, 100, 0] = float("nan")
+            bits[:, 255, -1] = float("inf")
+        y = gu.f32_out(2 * t, 256)
+        tb.tb_moe_down(w, gu.dev(qh), gu.dev(dqh), gu.dev(offsets), gu.dev(order), y)
+        out.append(gu.host(y))
+    hit = [0, 7, 100, 255]
+    assert not np.isfinite(out[1][:, hit]).any()
+    assert np.delete(out[1], hit, 1).tobytes() == np.delete(out[0], hit, 1).tobytes()
+
+
+def test_two_layers_at_once():
+    """Two streams, each with its own buffers, on the same experts."""
+    layer = layer_of(TERN, 8, 2048, 1024)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for x, t in enumerate((3, 60)):
+        q, dq = rows(t, 2048, 88 + x)
+        ids = ids_of("dropped", t, 4, 8, 90 + x)
+        runs.append((Run(layer, q, dq, ids), ids))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (run, _), s in zip(runs, streams):
+            run.launch(s)
+    torch.cuda.synchronize()
+    for run, ids in runs:
+        check(run, ids)
+
+
+def test_offsets_that_are_no_plan():
+    """Lists that overlap, so that there are more slots than pairs."""
+    layer = layer_of(TERN, 3, 640, 384)
+    for t in (9, 90):
+        q, dq = rows(t, 640, 92)
+        run = Run(layer, q, dq, ids_of("any", t, 2, 3, 93))
+        for bad in ([0, 2 * t, 0, 2 * t], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 2 ** 31 - 1], [5, 5, 5, 5]):
+            run.offsets.copy_(torch.tensor(bad, dtype=torch.int32))
+            run.order.copy_(torch.arange(2 * t, dtype=torch.int32).flip(0))
+            tb.tb_moe_gateup_silu(layer.gate, layer.up, run.q, run.dq, 2, run.offsets, run.order, run.h, run.qh, run.dqh)
+            tb.tb_moe_down(layer.down, run.qh, run.dqh, run.offsets, run.order, run.y)
+    torch.cuda.synchronize()
+
+
 def test_offsets_out_of_range_are_cut():
     """A plan that did not come from tb_moe_plan touches nothing past the arrays."""
     layer = Layer(TERN, 3, 256, 128, 77)
