@@ -340,6 +340,29 @@ def test_offsets_that_are_no_plan():
     torch.cuda.synchronize()
 
 
+def test_large_offsets():
+    """Codes, activations and rows of outputs past 4 GiB."""
+    experts, n, k, pairs = 66, 8320, 32768, 132000
+    gen = torch.Generator(device=gu.DEV).manual_seed(94)
+    codes = torch.randint(0, 256, (experts, n, k // 128, 32), dtype=torch.uint8, device=gu.DEV, generator=gen)
+    scales = torch.rand((experts, n, k // 128), device=gu.DEV, generator=gen).half()
+    qh = torch.randint(-127, 128, (pairs, k), dtype=torch.int8, device=gu.DEV, generator=gen)
+    dqh = torch.rand((pairs, k // 128), device=gu.DEV, generator=gen)
+    ids = torch.randint(0, experts, (pairs, 1), dtype=torch.int32, device=gu.DEV, generator=gen)
+    offsets, order = gu.i32_out(experts + 1), gu.i32_out(pairs)
+    y = torch.empty((pairs, n), device=gu.DEV)
+    tb.tb_moe_plan(ids, experts, offsets, order)
+    tb.tb_moe_down(tb.Experts(codes, scales, TERN), qh, dqh, offsets, order, y)
+    lists = offsets.tolist()
+    for e in (0, experts // 2, experts - 1):
+        one = tb.Matrix(codes[e], scales[e].view(torch.int16), n, k, TERN)
+        a, b = lists[e], lists[e + 1]
+        slots = torch.tensor([a, a + 1, (a + b) // 2, b - 1], device=gu.DEV)
+        want = gu.f32_out(4, n)
+        tb.tb_gemv_ternary(one, qh[slots].contiguous(), dqh[slots].contiguous(), want)
+        assert torch.equal(y[order[slots].long()], want), f"expert {e}"
+
+
 def test_offsets_out_of_range_are_cut():
     """A plan that did not come from tb_moe_plan touches nothing past the arrays."""
     layer = Layer(TERN, 3, 256, 128, 77)
