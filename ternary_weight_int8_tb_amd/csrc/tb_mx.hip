@@ -438,25 +438,36 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a)
     }
 }
 
-// y = the sum of the parts, in order.
-template <class T>
+// y = the sum of the parts, in order. VEC elements a thread (4, where rows of 4 fit), six parts' loads in
+// flight: a part after the other took 4.8 us for the 12 of 24 x 5120, 3.8 so.
+template <class T, int VEC>
 __global__ __launch_bounds__(256) void mx_sum_kernel(const float *__restrict__ part, size_t count, int parts, T *__restrict__ y)
 {
-    const size_t stride = (size_t)gridDim.x * 256 * 4;
-    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < count; i += stride) {
-        const int c = (int)(count - i < 4 ? count - i : 4);
+    constexpr int kLoads = 6;
+    const size_t stride = (size_t)gridDim.x * 256 * VEC;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * VEC; i < count; i += stride) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < parts; ++p) {
-            const float *q = part + (size_t)p * count + i;
-            if (c == 4 && ((uintptr_t)q & 15) == 0) {
-                const float4 x = *reinterpret_cast<const float4 *>(q);
-                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-            } else {
-                for (int e = 0; e < c; ++e)
-                    v[e] += q[e];
-            }
+        for (int p0 = 0; p0 < parts; p0 += kLoads) {
+            float x[kLoads][4] = {};
+#pragma unroll
+            for (int p = 0; p < kLoads; ++p)
+                if (p0 + p < parts) {   // the same for all lanes
+                    const float *q = part + (size_t)(p0 + p) * count + i;
+                    if (VEC == 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(q);
+                        x[p][0] = w.x, x[p][1] = w.y, x[p][2] = w.z, x[p][3] = w.w;
+                    } else {
+                        x[p][0] = *q;
+                    }
+                }
+#pragma unroll
+            for (int p = 0; p < kLoads; ++p)
+                if (p0 + p < parts)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        v[e] += x[p][e];
         }
-        put4(y + i, v, c);
+        put4(y + i, v, VEC);
     }
 }
 
@@ -476,9 +487,12 @@ MxPlan plan_gemm(int m, int n, int k)
         return {0, 0, 1};
     if (tile_count(m, n, 4, 4) >= 192)
         return {4, 4, 1};
-    const int tj = m <= 64 ? 1 : 2, groups = (k + kGroup - 1) / kGroup;
-    const int64_t tiles = tile_count(m, n, 2, tj);
-    return {2, tj, (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tiles), std::max(1, groups / 2))};
+    // 128 x 64 tiles while they are few; k in parts until there are two workgroups for each CU, or one where
+    // the parts' sums are many (24 x 5120 x 17408: 15.1 us in 6 parts, 14.3 in 12; 256 x 5120 x 5120: 17.2 in 3, 16.7 in 1;
+    // 509 x 5120 x 4096: 21.6 as 128 x 128 in 3 parts, 16.3 as 128 x 64 in 1; 512 x 9216 x 5120: 25.4 and 27.9)
+    const int tj = tile_count(m, n, 2, 1) <= 512 ? 1 : 2, groups = (k + kGroup - 1) / kGroup;
+    const int64_t tiles = tile_count(m, n, 2, tj), most = m <= 64 ? 512 : 256;
+    return {2, tj, (int)std::min<int64_t>(std::max<int64_t>(1, most / tiles), std::max(1, groups / 2))};
 }
 
 template <class T>
@@ -498,8 +512,12 @@ int launch_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, 
             return TB_EHIP;
         if (plan.parts > 1) {
             const size_t count = (size_t)m * w->n;
-            hipLaunchKernelGGL(mx_sum_kernel<T>, dim3((unsigned)std::min<size_t>((count + 1023) / 1024, kMaxGrid)), dim3(256), 0, stream,
-                               part, count, plan.parts, y);
+            const int each = count % 4 ? 256 : 1024;   // elements of a workgroup
+            const dim3 sums((unsigned)std::min<size_t>((count + each - 1) / each, kMaxGrid));
+            if (count % 4)
+                hipLaunchKernelGGL((mx_sum_kernel<T, 1>), sums, dim3(256), 0, stream, part, count, plan.parts, y);
+            else
+                hipLaunchKernelGGL((mx_sum_kernel<T, 4>), sums, dim3(256), 0, stream, part, count, plan.parts, y);
         }
         return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
     }

@@ -151,6 +151,14 @@ def test_gemm(m, n, k, dtype):
     assert torch.equal(gemm(ac, asc, wc, ws, TYPES[dtype]), y)
 
 
+# enough tiles for those of 128 x 128 and of 256 x 256, with rows, columns and groups of k that end inside one
+@pytest.mark.parametrize("m,n,k", [(513, 8328, 384), (1030, 10001, 640), (1537, 9000, 256)])
+def test_gemm_large_tiles(m, n, k):
+    test_gemm_exact(m, n, k)
+    for dtype in TYPES:
+        test_gemm(m, n, k, dtype)
+
+
 @pytest.mark.parametrize("m", [1, 20, 64, 300])
 def test_gemm_large_scales_and_nan(m):
     k, n = 512, 48
