@@ -84,6 +84,23 @@ def test_norm(m, k, dtype):
     check(x, res, gamma, 1e-6, o.s, o.y, o.q, o.dq)
 
 
+# more rows than workgroups are launched, in one to four passes over a row
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,k", [(8300, 128), (5500, 1280), (1100, 8192), (1100, 8320), (600, 17408), (700, 24704)])
+def test_norm_many_rows(m, k, dtype):
+    print(f"norm m={m} k={k} {dtype}", flush=True)
+    dt = TYPES[dtype]
+    x, res = rows(m, k, dt, 11), rows(m, k, dt, 12)
+    gamma = 1 + 0.3 * torch.randn(k, device=gu.DEV)
+    o = Out(m, k, dt)
+    tb.tb_add_rmsnorm_quant_i8(x, res, gamma, 1e-6, o.s, o.y, o.q, o.dq)
+    check(x, res, gamma, 1e-6, o.s, o.y, o.q, o.dq)
+    # in place, without y: the same codes
+    q, dq = o.q.clone(), o.dq.clone()
+    tb.tb_add_rmsnorm_quant_i8(x, res, gamma, 1e-6, res, None, o.q, o.dq)
+    assert torch.equal(o.q, q) and torch.equal(o.dq, dq) and torch.equal(res, o.s)
+
+
 @pytest.mark.parametrize("has_res,has_out,has_y", [(r, o, y) for r in (0, 1) for o in (0, 1) for y in (0, 1)])
 def test_norm_optional_arrays(has_res, has_out, has_y):
     m, k = 5, 1280
