@@ -39,10 +39,10 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const int32_t *_
                                                                 int32_t *__restrict__ order)
 {
     __shared__ int less_s[kPlanWaves], same_s[kPlanWaves];
-    const int e = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int e = blockIdx.x, waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     // each wave takes a contiguous range of whole groups of 256 ids, lane l ids 4 l .. 4 l + 3
-    const int groups = (pairs - 1) / 256 + 1;
-    const int g0 = part_lo(groups, kPlanWaves, wave), g1 = part_lo(groups, kPlanWaves, wave + 1);
+    const unsigned groups = (pairs - 1) / 256 + 1;   // below 2^23: times 16 waves, it fits
+    const int g0 = groups * wave / waves, g1 = groups * (wave + 1) / waves;
     auto read = [&](int g, int (&id)[4]) {
         const int64_t p = (int64_t)g * 256 + lane * 4;
         if (g < g1 && p + 4 <= pairs) {
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const int32_t *_
     }
     __syncthreads();
     int start = 0, before = 0;
-    for (int w = 0; w < kPlanWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
         start += less_s[w];
         before += w < wave ? same_s[w] : 0;
     }
@@ -1054,8 +1054,9 @@ int tb_moe_plan(const int32_t *ids, int tokens, int topk, int experts, int32_t *
     const tbh::Arg a[] = {{ids, (size_t)pairs * 4, false}, {offsets, (size_t)(experts + 1) * 4, true}, {order, (size_t)pairs * 4, true}};
     if ((rc = tbh::check_args(a)))
         return rc;
-    hipLaunchKernelGGL(moe_plan_kernel, dim3(experts + 1), dim3(kPlanThreads), 0, static_cast<hipStream_t>(stream), ids, pairs,
-                       experts, offsets, order);
+    const int waves = std::min(kPlanWaves, (pairs - 1) / 256 + 1);
+    hipLaunchKernelGGL(moe_plan_kernel, dim3(experts + 1), dim3(64 * waves), 0, static_cast<hipStream_t>(stream), ids, pairs, experts,
+                       offsets, order);
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
