@@ -255,9 +255,10 @@ struct MoeArgs {
 //     weight row i. So a lane folds the row whose codes and scales it loaded itself. Pair t of
 //     16 is A row 4 (t % 4) + t / 4: element e of lane group g is pair g + 4 e, and a tile of up to
 //     4 pairs folds one element.
-//   * A wave owns tiles of 16 weight rows through all of k; nothing of a row crosses waves. The blocks of a step are taken in the order in which the
-//     step's tree adds them: 0, last, last - 1, last - 2, then the next four downwards. Such a phase
-//     of 4 blocks leaves one partial sum, the tree above it one register set per level.
+//   * A wave owns tiles of 16 weight rows through all of k; nothing of a row crosses waves. The
+//     blocks of a step are taken in the order in which the step's tree adds them: 0, last, last - 1,
+//     last - 2, then the next four downwards. Such a phase of 4 blocks leaves one partial sum, the tree
+//     above it one register set per level.
 //   * Activations are staged in LDS as the operands read them: byte-transposed, 16 bytes per lane,
 //     in planes (block, instruction, lane group) of A rows.
 //   * Blocks past the end of k have dq = 0 and count +0.
@@ -288,16 +289,18 @@ __device__ __forceinline__ void stage_piece(uint8_t *lds, int u, int row, int un
     reinterpret_cast<v4i *>(lds)[(u * 8 + s * 4 + g) * T + (row ^ g)] = o;
 }
 
-// For the few-pairs kernel: the activations as the sum of two 8-bit floats (4 exponent bits), a
-// sign and half of the magnitude each: |q| = 16 h + l, and the bytes 0 .. 15 are the floats 0 .. 15 x 2^-9,
-// the numbers below 2^-6 and the binade from there on alike. So one instruction of 128 (its matrices' scales are powers of two) multiplies a block by
-// weights of 4 bits, that cost a third of the operations that bytes cost to make, and its sums are
-// whole numbers below 2^24, exact in float32, that need no conversion. An operand's lane holds the 16-byte
-// chunks c = 0, 1, of lane groups 2 c + g / 2, their registers 2 (g % 2) and 2 (g % 2) + 1: piece s of lane group G
-// goes to plane (c, g) = (G / 2, 2 (G % 2) + s) of the block.
-// Rows 2 NE (t % 4) + 2 (t / 4) and the next hold pair t's lower and upper halves, so that both end in
-// one lane. Row r stands at r ^ 2 g: the pieces that a wave stages spread over the banks.
-// Sign: the weights are the 4-bit floats' negatives, so the activations' signs are turned.
+// For the few-pairs kernel: the activations as the sum of two 8-bit floats (4 exponent bits), each with
+// the sign and half of the magnitude: |q| = 16 h + l, and the bytes 0 .. 15 are the floats
+// 0 .. 15 x 2^-9, for the numbers below 2^-6 and the binade from there on are spaced alike. So one
+// instruction of 128 elements, whose operands carry powers of two as scales, multiplies a block by
+// 4-bit weights, which cost a third of the operations that bytes cost to make. Its sums are whole
+// numbers below 2^24, exact in fp32, and need no conversion.
+// The instruction's 8-bit operand: lane group g's 16-byte chunks c = 0, 1 meet the 4-bit registers
+// 2 (g % 2) and the next of lane group 2 c + g / 2. So piece s of lane group G goes to plane
+// (c, g) = (G / 2, 2 (G % 2) + s) of the block. Rows 2 NE (t % 4) + 2 (t / 4) and the next hold pair
+// t's lower and upper halves, so that both sums end in one lane. Row r stands at r ^ 2 g: the pieces
+// that a wave stages spread over the banks.
+// Sign: the 4-bit floats are the negatives of the weights, so the activations' signs are turned.
 template <int FMT, int NE>
 __device__ __forceinline__ void stage_split(uint8_t *lds, int u, int t, int unit, uint4 v)
 {
@@ -412,7 +415,7 @@ __device__ __forceinline__ bool take_item(const MoeArgs &a, uint32_t b, int nblk
 
 // A step of the lane's row, loaded as a whole: 256 bytes of codes in four loads of 64 per row (loads of
 // a block, 8 bytes a lane, kept the address unit busy for 40% of the wide kernel's time, and
-// fetched each 128-byte line several times). codes[x] is bytes 64 x + 16 g .. + 15 of the step's 256, scales the step's.
+// fetched each 128-byte line several times). codes[x] is bytes 64 x + 16 g .. + 15 of the step's 256.
 template <int FMT>
 struct StepRow {
     static constexpr int kScaleWords = Core<FMT>::kStep / 2;
@@ -440,8 +443,9 @@ struct StepRow {
         }
         scales[kScaleWords] = buffer_load_u32(s, so + kScaleWords * 4);
     }
-    // After the loads, by lane swaps: each block's codes, 16 bytes of which one lane group loaded, in all groups, scales from bit 0 of scales[0] on.
-    // odd: the row's first scale is the upper half of its word; left: the blocks from this step's first on
+    // After the loads, by lane swaps: each block's codes, 16 bytes of which one lane group loaded, in
+    // all groups; scales from bit 0 of scales[0] on.
+    // odd: the row's first scale is the upper half of its word; left: blocks from this step's first on
     __device__ __forceinline__ void deal(bool odd, int left)
     {
 #pragma unroll
@@ -696,11 +700,14 @@ __global__ __launch_bounds__(1024) void moe_wide_kernel(MoeArgs a, uint32_t firs
 }
 
 // ------------------------------------------------------------------------------------
-// Few pairs per expert: tiles of 8 pairs, 8 waves of 16 weight rows. Here the operations that make
-// operands of the codes count most, for they serve 8 pairs at most, so the product is of 4-bit by 8-bit floats (stage_split): at
-// 5 pairs of each of 16 experts, sign, 2 x 2176 x 5120, 40 us with bytes and tiles of 16 pairs of 4 waves, 27 us here. The
-// codes are loaded a step ahead. What bounds it: each unit of 16 rows by a block takes some 22 vector operations
-// and 2 KB read from LDS, and few workgroups leave the loads' and the staging's latency bare.
+// Few pairs per expert: tiles of 8 pairs, 8 waves of 16 weight rows. The operations that make operands
+// of the codes serve 8 pairs at most and count most here, so the product is of 4-bit by 8-bit floats
+// (stage_split). At 5 pairs of each of 16 experts, sign, k = 5120, gate/up of 2176 rows took 40 us, down
+// 34, as products of bytes in tiles of 16 pairs; 22 to 30 (by the longest lists) and 18 so. Codes are
+// loaded a step ahead. Bound: nothing alone. A unit of 16 rows by a block takes 22 vector
+// operations and 2 KB from LDS, and a workgroup spends about as long again on the chain of its first
+// loads (offsets, order, activations) and on staging. Two row tiles a wave, which halve what is
+// read from LDS, and loads by whole lines, which take lane exchanges, measured the same within 5%.
 // ------------------------------------------------------------------------------------
 template <int FMT, bool TWO>
 struct NarrowShape {
@@ -993,7 +1000,10 @@ int launch_items(int64_t tiles, int parts, F &&launch)
 // Tiles of `rows` pairs at most: every expert's last may be partly filled, and none is empty.
 int64_t most_tiles(const MoeArgs &a, int rows) { return std::min<int64_t>(a.pairs, (int64_t)a.pairs / rows + a.experts); }
 
-// Wide tiles from an average of 24 pairs per expert on.
+// Wide tiles from an average of 24 pairs per expert on. gate/up and down in narrow and wide tiles, us:
+// 16 experts, ternary, 2048 x 1024, 16 pairs each 20 + 12 and 22 + 16, 24 each 24 + 15 and 23 + 16, 32 each
+// 27 + 17 and 23 + 17; sign, 5120 x 2176, 24 each 75 + 43 and 101 + 67, 64 each 156 + 95 and 147 + 124; 64 experts,
+// ternary, 5120 x 2176, 16 each 168 + 102 and 183 + 109, 24 each 237 + 142 and 203 + 140.
 bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)experts * 24; }
 
 template <int FMT, bool TWO>

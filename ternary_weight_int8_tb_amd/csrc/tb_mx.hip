@@ -205,7 +205,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void mx_rows_kernel(const uint8_t *
 //     Block j of row r lies at place j ^ ((r / 2) % 8) of the row's 8, so that the 16 lanes that one
 //     LDS cycle serves read 16 different columns of banks. A group's scales go the same way.
 // Bound: matrix rate. Per 64 elements of k a wave's TI TJ instructions take 32 TI TJ cycles and TI + TJ
-// reads of 1 KB: at 4 x 4 all four waves read 64 bytes a cycle of the 128 that LDS gives.
+// reads of 1 KB: at 4 x 4 all four waves read 64 bytes a cycle of the 128 that LDS gives. Measured:
+// 8192 x 17408 x 5120 430 to 480 us, 3.0 to 3.4 PFLOP/s; the instruction alone, on random codes, runs at
+// 6.6 to 7.5 (9.9 on zeros: power bounds it).
 // ------------------------------------------------------------------------------------
 constexpr int kGroup = 512;              // elements of k whose scales are loaded together
 constexpr uint32_t kBufWord3 = 0x00020000u;
@@ -487,9 +489,10 @@ MxPlan plan_gemm(int m, int n, int k)
         return {0, 0, 1};
     if (tile_count(m, n, 4, 4) >= 192)
         return {4, 4, 1};
-    // 128 x 64 tiles while they are few; k in parts until there are two workgroups for each CU, or one where
-    // the parts' sums are many (24 x 5120 x 17408: 15.1 us in 6 parts, 14.3 in 12; 256 x 5120 x 5120: 17.2 in 3, 16.7 in 1;
-    // 509 x 5120 x 4096: 21.6 as 128 x 128 in 3 parts, 16.3 as 128 x 64 in 1; 512 x 9216 x 5120: 25.4 and 27.9)
+    // 128 x 64 tiles while they are few; k in parts until there are two workgroups for each CU, or one
+    // where the parts' sums are many (24 x 5120 x 17408: 15.1 us in 6 parts, 14.3 in 12;
+    // 256 x 5120 x 5120: 17.2 in 3, 16.7 in 1; 509 x 5120 x 4096: 21.6 as 128 x 128 in 3 parts, 16.3 as
+    // 128 x 64 in 1; 512 x 9216 x 5120: 25.4 as 128 x 128 and 27.9 as 128 x 64)
     const int tj = tile_count(m, n, 2, 1) <= 512 ? 1 : 2, groups = (k + kGroup - 1) / kGroup;
     const int64_t tiles = tile_count(m, n, 2, tj), most = m <= 64 ? 512 : 256;
     return {2, tj, (int)std::min<int64_t>(std::max<int64_t>(1, most / tiles), std::max(1, groups / 2))};
