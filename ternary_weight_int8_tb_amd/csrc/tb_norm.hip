@@ -52,7 +52,7 @@ __device__ __forceinline__ void add_rows(const Eight<T> &x, const Eight<T> &res,
 __device__ __forceinline__ uint2 codes(const float (&u)[8], float amax, float sign)
 {
     uint32_t w[2] = {0u, 0u};
-    if (amax >= kZeroBlock) {
+    if (amax >= kZeroBlock && amax < INFINITY) {
         const float inv = (127.0f / amax) * sign;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -84,7 +84,7 @@ __device__ __forceinline__ float norm_of(const double *part, int waves, int k, f
     for (int w = 0; w < waves; ++w)
         total += part[w];
     const double mean = total / (double)k + (double)eps;
-    return mean > 0.0 ? (float)(1.0 / sqrt(mean)) : 0.0f;   // a row of zeros, eps = 0
+    return mean == 0.0 ? 0.0f : (float)(1.0 / sqrt(mean));   // 0: a row of zeros, eps = 0
 }
 
 // Rows of up to 64 blocks: a lane's 8 elements of a row stay in registers until y, those of gamma for
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
         if (on)
             *reinterpret_cast<uint2 *>(q + i) = c;
         if (lane16 == 0)
-            amax_s[turn][b] = amax >= kZeroBlock ? amax : 0.0f;
+            amax_s[turn][b] = amax < kZeroBlock ? 0.0f : amax;   // a NaN stays
         __syncthreads();
         if (tid >= 64 && !y)
             continue;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
             const float amax = __uint_as_float(amax_bits<4>(v));
             *reinterpret_cast<uint2 *>(q + i) = codes(v, amax, sign);
             if (lane16 == 0)
-                amax_s[b] = amax >= kZeroBlock ? amax : 0.0f;
+                amax_s[b] = amax < kZeroBlock ? 0.0f : amax;
         }
         sum = wave_sum(sum);
         if ((tid & 63) == 0)

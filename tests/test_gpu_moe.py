@@ -308,6 +308,21 @@ def test_scales_that_are_not_finite_stay_in_their_row(fmt, t, k):
     assert np.delete(out[1], hit, 1).tobytes() == np.delete(out[0], hit, 1).tobytes()
 
 
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("t", [7, 90])
+def test_rows_that_are_not_finite_stay_alone(fmt, t):
+    """A token whose scales are NaN or infinite changes no other token's rows."""
+    layer = layer_of(fmt, 3, 640, 384)
+    q, dq = rows(t, 640, 95)
+    ids = ids_of("any", t, 2, 3, 96)
+    clean = Run(layer, q, dq, ids).launch()
+    bad = dq.copy()
+    bad[2], bad[t - 1, 0] = np.nan, np.inf
+    run = Run(layer, q, bad, ids).launch()
+    good = [x for x in range(t) if x not in (2, t - 1)]
+    assert torch.equal(run.out[good], clean.out[good])
+
+
 def test_two_layers_at_once():
     """Two streams, each with its own buffers, on the same experts."""
     layer = layer_of(TERN, 8, 2048, 1024)

@@ -144,6 +144,47 @@ def test_norm_zero_and_tiny_rows():
     assert not gu.host(o.y)[0].any() and not gu.host(o.dq)[0].any()
 
 
+@pytest.mark.parametrize("k", [512, 8320])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_rows_that_are_not_finite(k, dtype):
+    m, dt = 6, TYPES[dtype]
+    x, gamma = rows(m, k, dt, 21), 1 + 0.3 * torch.randn(k, device=gu.DEV)
+    clean = Out(m, k, dt)
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 1e-6, None, clean.y, clean.q, clean.dq)
+    x[1, 130], x[3, 5], x[4, k - 1] = float("nan"), float("inf"), float("-inf")
+    o = Out(m, k, dt)
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 1e-6, None, o.y, o.q, o.dq)
+    good = [0, 2, 5]
+    for a, b in ((o.q, clean.q), (o.dq, clean.dq), (o.y, clean.y)):
+        assert torch.equal(a[good], b[good])
+    assert torch.isnan(o.dq[1]).all() and torch.isnan(o.y[1]).all()
+    for row, block in ((1, 1), (3, 0), (4, k // 128 - 1)):
+        assert torch.isnan(o.dq[row, block]) and not o.q[row, 128 * block:128 * (block + 1)].any()
+    for row, block in ((3, 0), (4, k // 128 - 1)):   # the mean is infinite: f = 0
+        others = [b for b in range(k // 128) if b != block]
+        assert not o.dq[row, others].any()
+
+
+def test_norm_large_offsets():
+    """Rows past 4 GiB have the bits that they have alone."""
+    m, k = 270003, 8192
+    x = torch.empty(m, k, dtype=torch.bfloat16, device=gu.DEV).normal_()
+    gamma = 1 + 0.3 * torch.randn(k, device=gu.DEV)
+    s, q, dq = torch.empty_like(x), gu.i8_out(m, k), gu.f32_out(m, k // 128)
+    tb.tb_add_rmsnorm_quant_i8(x, x, gamma, 1e-6, s, None, q, dq)
+    codes = torch.empty(m, k // 2, dtype=torch.uint8, device=gu.DEV)
+    scales = torch.empty(m, k // 32, dtype=torch.uint8, device=gu.DEV)
+    tb.tb_mxfp4_quant(s, codes, scales, True)
+    for a in (0, 131071, m - 3):
+        part = x[a:a + 3].clone()
+        s2, q2, dq2 = torch.empty_like(part), gu.i8_out(3, k), gu.f32_out(3, k // 128)
+        tb.tb_add_rmsnorm_quant_i8(part, part, gamma, 1e-6, s2, None, q2, dq2)
+        c2, sc2 = torch.empty_like(codes[:3]), torch.empty_like(scales[:3])
+        tb.tb_mxfp4_quant(s2, c2, sc2, True)
+        for all_rows, alone in ((s, s2), (q, q2), (dq, dq2), (codes, c2), (scales, sc2)):
+            assert torch.equal(all_rows[a:a + 3], alone)
+
+
 def test_norm_codes_are_those_of_the_quantiser():
     # gamma = 1, no residual: the codes of tb_rotate_quant_i8 on the same rows
     x = rows(8, 5120, torch.float32, 7)
