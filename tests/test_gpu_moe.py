@@ -378,6 +378,30 @@ def test_large_offsets():
         assert torch.equal(y[order[slots].long()], want), f"expert {e}"
 
 
+def test_more_items_than_a_launch_holds():
+    """Over 2^20 workgroups: 40000 experts of 32 row groups, about one pair each."""
+    experts, n, k, pairs = 40000, 4096, 128, 40000
+    gen = torch.Generator(device=gu.DEV).manual_seed(97)
+    codes = torch.randint(0, 256, (experts, n, 1, 16), dtype=torch.uint8, device=gu.DEV, generator=gen)
+    scales = torch.rand((experts, n, 1), device=gu.DEV, generator=gen).half()
+    qh = torch.randint(-127, 128, (pairs, k), dtype=torch.int8, device=gu.DEV, generator=gen)
+    dqh = torch.rand((pairs, 1), device=gu.DEV, generator=gen)
+    ids = torch.randint(0, experts, (pairs, 1), dtype=torch.int32, device=gu.DEV, generator=gen)
+    offsets, order = gu.i32_out(experts + 1), gu.i32_out(pairs)
+    y = gu.f32_out(pairs, n)
+    tb.tb_moe_plan(ids, experts, offsets, order)
+    tb.tb_moe_down(tb.Experts(codes, scales, SIGN), qh, dqh, offsets, order, y)
+    lists = gu.host(offsets)
+    assert np.array_equal(lists, np.searchsorted(np.sort(gu.host(ids)[:, 0]), np.arange(experts + 1)))
+    assert not torch.isnan(y).any()
+    for e in np.nonzero(np.diff(lists))[0][[0, 1000, 20000, -1]]:
+        one = tb.Matrix(codes[e], scales[e].view(torch.int16), n, k, SIGN)
+        slot = int(lists[e])
+        want = gu.f32_out(1, n)
+        tb.tb_gemv_ternary(one, qh[slot:slot + 1].clone(), dqh[slot:slot + 1].clone(), want)
+        assert torch.equal(y[order[slot].long()], want[0]), f"expert {e}"
+
+
 def test_offsets_out_of_range_are_cut():
     """A plan that did not come from tb_moe_plan touches nothing past the arrays."""
     layer = Layer(TERN, 3, 256, 128, 77)
