@@ -584,9 +584,12 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
             w.deal(rows.soff & 2, nb - step * C::kStep);
 #pragma unroll
             for (int j = 0; j < S::kPhases; ++j) {
-                float sum[NT][4];
+                float sum[NT][4] = {};
+                // A phase past the end is left out (sign, 8 blocks of 16: 338 us to 296; half phases to 276, but
+                // rows of whole steps 5% slower). The first holds block 0, the last makes room for the next codes.
+                const bool any = j == 0 || j == S::kPhases - 1 || C::kStep - 4 * j - 3 < nb - step * C::kStep;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {   // two blocks of the phase
+                for (int h = 0; any && h < 2; ++h) {   // two blocks of the phase
                     int blk[2];
                     v4i wt[2][2];
                     float s[2];
@@ -815,9 +818,9 @@ __device__ __forceinline__ void narrow_product(const MoeArgs &a, const Tile &til
 #pragma unroll
                 for (int q = 0; q < S::kPhases; ++q) {
                     float sum[NE] = {};
-                    if (q == 0 || C::kStep - 4 * q - 3 < left) {   // else all of its blocks are past the end
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < 2; ++h) {
+                        if ((q == 0 && h == 0) || C::kStep - (4 * q + 2 * h + 1) < left) {   // else both are past the end
                             float term[2][NE];
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
