@@ -1006,27 +1006,50 @@ int launch_items(int64_t tiles, int parts, F &&launch)
 // Tiles of `rows` pairs at most: every expert's last may be partly filled, and none is empty.
 int64_t most_tiles(const MoeArgs &a, int rows) { return std::min<int64_t>(a.pairs, (int64_t)a.pairs / rows + a.experts); }
 
-// Wide tiles from an average of 24 pairs per expert on. gate/up and down in narrow and wide tiles, us:
-// 16 experts, ternary, 2048 x 1024, 16 pairs each 20 + 12 and 22 + 16, 24 each 24 + 15 and 23 + 16, 32 each
-// 27 + 17 and 23 + 17; sign, 5120 x 2176, 24 each 75 + 43 and 101 + 67, 64 each 156 + 95 and 147 + 124; 64 experts,
-// ternary, 5120 x 2176, 16 each 168 + 102 and 183 + 109, 24 each 237 + 142 and 203 + 140.
-bool wide_tiles(int pairs, int experts) { return (int64_t)pairs >= (int64_t)experts * 24; }
+// Wide tiles from this many pairs per expert on, on the average: earlier for ternary codes, whose
+// decode costs the narrow tiles more, and where the experts' row groups fill the chip. gate/up + down in
+// narrow and in wide tiles, us, by pairs per expert: 16 experts, ternary, 2048 x 1024, 16: 32 and 38, 24: 38 and 38,
+// 32: 44 and 39; 64 experts, 16: 75 and 57, 24: 103 and 85; 16 experts, sign, 5120 x 2176, 24: 110 and 154, 32: 137
+// and 153, 48: 188 and 156; 64 experts, sign, 2048 x 1024, 24: 101 and 106, 32: 124 and 94.
+bool wide_tiles(const MoeArgs &a, int fmt)
+{
+    const bool full = (int64_t)a.experts * ((a.n + 127) / 128) >= 512;
+    return (int64_t)a.pairs >= (int64_t)a.experts * (fmt == TB_FMT_TERNARY2 ? (full ? 16 : 24) : (full ? 28 : 36));
+}
+
+// Into how many workgroups a tile's row groups go. A CU holds one; to start and to stage takes it the time
+// of some 11 blocks of a row group (10 us), which speaks for few, and what counts is the rounds that they
+// make on 256 CUs. tiles: about half a tile per expert is not full. gate/up in us, as few parts as leave two
+// workgroups for each CU, and so: 147 tiles x 5 groups x 28 blocks 165 and 96; 51 x 8 x 16 39 and 33;
+// 29 x 17 x 40 (sign) 147 and 103; 218 x 4 x 9 (sign) 63 and 56; 117 x 17 x 40 329 and 298, 64 x 17 x 40 203
+// and 236; 715 x 8 x 16 one part both ways, 290 (in 2 349, in 8 422).
+int wide_groups(int64_t tiles, int nblk, int blocks)
+{
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int p = 1; p <= nblk && p <= 256; ++p) {
+        const int64_t cost = (tiles * p + 255) / 256 * (11 + (int64_t)blocks * ((nblk + p - 1) / p));
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
+}
 
 template <int FMT, bool TWO>
 int launch_product_as(const MoeArgs &a, hipStream_t stream)
 {
-    if (!wide_tiles(a.pairs, a.experts)) {
+    if (!wide_tiles(a, FMT)) {
         using S = NarrowShape<FMT, TWO>;
         return launch_items(most_tiles(a, S::kT), (a.n + S::kCols - 1) / S::kCols, [&](dim3 grid, uint32_t first) {
             hipLaunchKernelGGL((moe_narrow_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first);
         });
     }
     using S = WideShape<FMT, TWO>;
-    // a tile's row groups go to as few workgroups as leave two for each CU: little is staged twice
-    // (at 715 tiles of 8 row groups, gate/up: 330 us in 1 part each, 349 in 2, 371 in 4, 422 in 8)
     const int64_t tiles = most_tiles(a, S::kT);
-    const int nblk = (a.n + S::kCols - 1) / S::kCols;
-    const int groups = (int)std::min<int64_t>(nblk, (512 + tiles - 1) / tiles);
+    const int nblk = (a.n + S::kCols - 1) / S::kCols, steps = (a.k / kBlock + Core<FMT>::kStep - 1) / Core<FMT>::kStep;
+    const int groups = wide_groups(a.pairs / S::kT + (a.experts + 1) / 2, nblk, steps * Core<FMT>::kStep);
     return launch_items(tiles, groups, [&](dim3 grid, uint32_t first) {
         hipLaunchKernelGGL((moe_wide_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first, groups);
     });
@@ -1096,7 +1119,7 @@ int tb_moe_gateup_silu(const tb_experts *wg, const tb_experts *wu, const int8_t 
     const MoeArgs args = {{static_cast<const uint8_t *>(wg->codes), static_cast<const uint8_t *>(wu->codes)},
                           {wg->scales, wu->scales}, wg->experts, wg->n, wg->k, q, dq, offsets, order, (int)pairs, topk, h, qh, dqh,
                           tbh::dq_unit()};
-    if ((rc = launch_product<true>(args, wg->fmt, st)) || wide_tiles((int)pairs, wg->experts))
+    if ((rc = launch_product<true>(args, wg->fmt, st)) || wide_tiles(args, wg->fmt))
         return rc;
     const size_t blocks = pairs * (n / kBlock);
     const int grid = (int)std::min<size_t>((blocks + kRotThreads / 16 - 1) / (kRotThreads / 16), kMaxGrid);
