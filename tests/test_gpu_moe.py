@@ -153,6 +153,16 @@ def test_moe_long_rows(fmt):
 
 
 @pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("kind", ["distinct", "one", "dropped"])
+def test_moe_long_rows_of_many_pairs(fmt, kind):
+    layer = layer_of(fmt, 2, 128 * 37, 128 * 21)
+    t = 130
+    q, dq = rows(t, layer.hidden, 98)
+    ids = ids_of(kind, t, 2, 2, 99)
+    check(Run(layer, q, dq, ids).launch(), ids)
+
+
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
 def test_moe_against_the_oracle(fmt):
     layer = Layer(fmt, 3, 512, 256, 67)
     q, dq = rows(11, 512, 68)
