@@ -477,15 +477,17 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(const float *__restrict__ p
 struct MxPlan {
     int ti, tj, parts;
 };
-// Up to 8 rows of up to 8192 elements one launch of the row kernel; the tiles, which stream the weights
-// through LDS in whole lines, need a second launch for the sums. Measured, us a call, row kernel and
-// tiles: 1 x 9216 x 5120 9.1 and 10.6, 8 x 9216 x 5120 10.4 and 11.2, 16 x 9216 x 5120 12.3 and 11.0,
-// 1 x 5120 x 17408 16.4 and 15.0, 24 x 5120 x 17408 33 and 16.7.
+// Up to 8 rows of up to 8192 elements, and 2^20 x 48 weights: one launch of the row kernel; the tiles, which
+// stream the weights through LDS in whole lines, need a second launch for the sums. Measured, us a call,
+// row kernel and tiles: 1 x 5120 x 4096 6.6 and 9.8, 1 x 9216 x 5120 8.8 and 9.5, 8 x 9216 x 5120 10.5 and
+// 10.0, 16 x 9216 x 5120 12.2 and 10.2, 1 x 17408 x 5120 13.7 and 13.2, 8 x 17408 x 5120 16.3 and 13.6,
+// 1 x 5120 x 17408 16.5 and 12.8.
 constexpr int kRowsMost = 8, kRowsMostK = 8192;
+constexpr int64_t kRowsMostWeights = 48 << 20;
 int64_t tile_count(int m, int n, int ti, int tj) { return (int64_t)((m + 64 * tj - 1) / (64 * tj)) * ((n + 64 * ti - 1) / (64 * ti)); }
 MxPlan plan_gemm(int m, int n, int k)
 {
-    if (m <= kRowsMost && k <= kRowsMostK)
+    if (m <= kRowsMost && k <= kRowsMostK && (int64_t)n * k <= kRowsMostWeights)
         return {0, 0, 1};
     if (tile_count(m, n, 4, 4) >= 192)
         return {4, 4, 1};
