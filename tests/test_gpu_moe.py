@@ -215,10 +215,11 @@ def test_plan(pairs_topk_experts):
     assert np.array_equal(gu.host(offsets), np.concatenate([[0], np.cumsum(counts)]))
 
 
-def test_moe_graph_and_streams():
+@pytest.mark.parametrize("t", [50, 150])   # tiles of few and of many pairs
+def test_moe_graph_and_streams(t):
     """A captured pass follows its inputs from replay to replay; two layers run on two streams at once."""
     layer = Layer(TERN, 6, 512, 256, 72)
-    t, topk = 50, 2
+    topk = 2
     q, dq = rows(t, 512, 73)
     run = Run(layer, q, dq, ids_of("any", t, topk, 6, 74))
     run.launch()
@@ -242,6 +243,7 @@ def test_moe_graph_and_streams():
     for _ in range(3):
         for run, s in zip(runs, streams):
             run.launch(s)
+    torch.cuda.synchronize()
     for run, i in zip(runs, ids):
         check(run, i)
 
