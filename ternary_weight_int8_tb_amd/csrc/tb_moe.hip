@@ -1008,27 +1008,30 @@ int64_t most_tiles(const MoeArgs &a, int rows) { return std::min<int64_t>(a.pair
 
 // Wide tiles from this many pairs per expert on, on the average: earlier for ternary codes, whose
 // decode costs the narrow tiles more, and where the experts' row groups fill the chip. gate/up + down in
-// narrow and in wide tiles, us, by pairs per expert: 16 experts, ternary, 2048 x 1024, 16: 32 and 38, 24: 38 and 38,
-// 32: 44 and 39; 64 experts, 16: 75 and 57, 24: 103 and 85; 16 experts, sign, 5120 x 2176, 24: 110 and 154, 32: 137
-// and 153, 48: 188 and 156; 64 experts, sign, 2048 x 1024, 24: 101 and 106, 32: 124 and 94.
+// narrow and in wide tiles, us, by pairs per expert: 16 experts, ternary, 2048 x 1024, 16: 32 and 37, 24: 38
+// and 38, 32: 44 and 39; 64 experts, 12: 62 and 56, 16: 75 and 58, 24: 103 and 73; 64 experts, 5120 x 2176, 12: 222
+// and 266, 16: 280 and 271; 16 experts, sign, 5120 x 2176, 24: 110 and 154, 32: 137 and 155, 48: 188 and 156;
+// 64 experts, sign, 2048 x 1024, 24: 101 and 93, 32: 124 and 94.
 bool wide_tiles(const MoeArgs &a, int fmt)
 {
     const bool full = (int64_t)a.experts * ((a.n + 127) / 128) >= 512;
-    return (int64_t)a.pairs >= (int64_t)a.experts * (fmt == TB_FMT_TERNARY2 ? (full ? 16 : 24) : (full ? 28 : 36));
+    return (int64_t)a.pairs >= (int64_t)a.experts * (fmt == TB_FMT_TERNARY2 ? (full ? 14 : 24) : (full ? 28 : 36));
 }
 
 // Into how many workgroups a tile's row groups go. A CU holds one; to start and to stage takes it the time
 // of some 11 blocks of a row group (10 us), which speaks for few, and what counts is the rounds that they
-// make on 256 CUs. tiles: about half a tile per expert is not full. gate/up in us, as few parts as leave two
-// workgroups for each CU, and so: 147 tiles x 5 groups x 28 blocks 165 and 96; 51 x 8 x 16 39 and 33;
-// 29 x 17 x 40 (sign) 147 and 103; 218 x 4 x 9 (sign) 63 and 56; 117 x 17 x 40 329 and 298, 64 x 17 x 40 203
-// and 236; 715 x 8 x 16 one part both ways, 290 (in 2 349, in 8 422).
+// make on 256 CUs, a last one that is not full by half, for tiles that are not full are faster. tiles: one
+// per expert, or about half a tile of each not full and some more. gate/up in us, as few parts as leave two
+// workgroups for each CU, and so: 147 tiles x 5 groups x 28 blocks 165 and 87; 51 x 8 x 16 39 and 33;
+// 31 x 17 x 40 (sign) 147 and 103; 218 x 4 x 9 (sign) 63 and 54; 125 x 17 x 40 329 and 296, 72 x 17 x 40 203
+// and 200; 722 x 8 x 16 one part both ways, 290 (in 2 349, in 8 422).
 int wide_groups(int64_t tiles, int nblk, int blocks)
 {
     int best = 1;
     int64_t least = INT64_MAX;
     for (int p = 1; p <= nblk && p <= 256; ++p) {
-        const int64_t cost = (tiles * p + 255) / 256 * (11 + (int64_t)blocks * ((nblk + p - 1) / p));
+        const int64_t work = tiles * p, full = (work + 255) / 256 * 256;
+        const int64_t cost = (full + std::max<int64_t>(work, 256)) * (11 + (int64_t)blocks * ((nblk + p - 1) / p));
         if (cost < least) {
             least = cost;
             best = p;
@@ -1049,7 +1052,8 @@ int launch_product_as(const MoeArgs &a, hipStream_t stream)
     using S = WideShape<FMT, TWO>;
     const int64_t tiles = most_tiles(a, S::kT);
     const int nblk = (a.n + S::kCols - 1) / S::kCols, steps = (a.k / kBlock + Core<FMT>::kStep - 1) / Core<FMT>::kStep;
-    const int groups = wide_groups(a.pairs / S::kT + (a.experts + 1) / 2, nblk, steps * Core<FMT>::kStep);
+    const int likely = std::max(std::min(a.pairs, a.experts), a.pairs / S::kT + (a.experts * 5 + 7) / 8);
+    const int groups = wide_groups(likely, nblk, steps * Core<FMT>::kStep);
     return launch_items(tiles, groups, [&](dim3 grid, uint32_t first) {
         hipLaunchKernelGGL((moe_wide_kernel<FMT, TWO>), grid, dim3(S::kThreads), 0, stream, a, first, groups);
     });
