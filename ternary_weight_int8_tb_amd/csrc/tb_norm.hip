@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
             continue;
         const float r = norm_of(part_s[turn], waves, nb * kBlock, eps);
         if (tid < nb)   // the first wave's lanes
-            dq[row * nb + tid] = amax_s[turn][tid] != 0.0f ? amax_s[turn][tid] * (r * unit) : 0.0f;
+            dq[row * nb + tid] = amax_s[turn][tid] * (r * unit);   // r is finite, or the row holds a NaN
         if (y && on) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
         __syncthreads();
         const float r = norm_of(part_s, blockDim.x >> 6, nb * kBlock, eps);
         for (int b = tid; b < nb; b += blockDim.x)
-            dq[row * nb + b] = amax_s[b] != 0.0f ? amax_s[b] * (r * unit) : 0.0f;
+            dq[row * nb + b] = amax_s[b] * (r * unit);   // r is finite, or the row holds a NaN
 
         if (y)
             for (int b = tid >> 4; b < nb; b += groups) {

@@ -265,3 +265,15 @@ def test_norm_binding_refusals():
     call(dq=o.dq[:, :1])
     call(y=x)                      # y may not be an input
     assert (gu.host(o.q) == gu.POISON_I8).all()
+
+
+@pytest.mark.parametrize("k", [512, 8320])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_zero_block_of_a_row_with_a_nan(k, dtype):
+    x = rows(3, k, TYPES[dtype], 30)
+    x[1:, :128] = 0
+    x[1, k - 1] = float("nan")
+    o = Out(3, k, TYPES[dtype])
+    tb.tb_add_rmsnorm_quant_i8(x, None, torch.ones(k, device=gu.DEV), 1e-6, None, o.y, o.q, o.dq)
+    assert torch.isnan(o.dq[1]).all() and torch.isnan(o.y[1]).all() and not o.q[1, :128].any()
+    assert o.dq[2, 0] == 0 and (o.dq[2, 1:] > 0).all()   # without a NaN it stays a block of zeros
