@@ -65,6 +65,13 @@ __device__ __forceinline__ uint2 codes(const float (&u)[8], float amax, float si
     return make_uint2(w[0], w[1]);
 }
 
+// The block's amax in dq: 0 if it counts as zero, a NaN if it is not finite (infinite ones too: the
+// block has no codes).
+__device__ __forceinline__ float kept_amax(float amax)
+{
+    return amax < kZeroBlock ? 0.0f : amax < INFINITY ? amax : NAN;
+}
+
 // The sum over a wave's lanes, in every lane.
 __device__ __forceinline__ double wave_sum(double v)
 {
@@ -142,7 +149,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
         if (on)
             *reinterpret_cast<uint2 *>(q + i) = c;
         if (lane16 == 0)
-            amax_s[turn][b] = amax < kZeroBlock ? 0.0f : amax;   // a NaN stays
+            amax_s[turn][b] = kept_amax(amax);
         __syncthreads();
         if (tid >= 64 && !y)
             continue;
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
             const float amax = __uint_as_float(amax_bits<4>(v));
             *reinterpret_cast<uint2 *>(q + i) = codes(v, amax, sign);
             if (lane16 == 0)
-                amax_s[b] = amax < kZeroBlock ? 0.0f : amax;
+                amax_s[b] = kept_amax(amax);
         }
         sum = wave_sum(sum);
         if ((tid & 63) == 0)

@@ -277,3 +277,19 @@ def test_norm_zero_block_of_a_row_with_a_nan(k, dtype):
     tb.tb_add_rmsnorm_quant_i8(x, None, torch.ones(k, device=gu.DEV), 1e-6, None, o.y, o.q, o.dq)
     assert torch.isnan(o.dq[1]).all() and torch.isnan(o.y[1]).all() and not o.q[1, :128].any()
     assert o.dq[2, 0] == 0 and (o.dq[2, 1:] > 0).all()   # without a NaN it stays a block of zeros
+
+
+@pytest.mark.parametrize("k", [512, 8320])
+def test_norm_block_whose_rotation_overflows(k):
+    """Finite rows, u past the largest fp32: with infinities alone, and with NaN among them."""
+    x = rows(3, k, torch.float32, 31)
+    x[:2, :128] = 0
+    x[0, :4] = 1          # 4 x 1e38 is infinite, and nothing is subtracted from it
+    x[1, :8] = 1
+    gamma = torch.ones(k, device=gu.DEV)
+    gamma[:128] = 1e38
+    x[2, :128] = 0
+    o = Out(3, k, torch.float32)
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 1e-6, None, o.y, o.q, o.dq)
+    assert torch.isnan(o.dq[:2, 0]).all() and not o.q[:, :128].any() and o.dq[2, 0] == 0
+    assert torch.isfinite(o.dq[:, 1:]).all() and torch.isfinite(o.y).all()
