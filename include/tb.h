@@ -368,8 +368,9 @@ enum tb_dtype { TB_F32 = 0, TB_BF16 = 1, TB_F16 = 2 };
  * q*dq approximates the orthonormal rotation of the normed row, as tb_rotate_quant_i8 on it
  * would. f scales whole blocks, so it enters dq and not q. A block with amax < 2^-100 counts as
  * amax = 0, with q = 0. A row of zeros with eps = 0 has f = 0. A block whose u are not all finite has q = 0
- * and dq a NaN; a row that holds a NaN has f, y and every dq so, of blocks of zeros too. Squares are summed in fp32 over 8
- * elements at a time: above about 2^61 they overflow, and f is 0. Any number of rows.
+ * and dq a NaN; a row that holds a NaN has f, y and every dq so, of blocks of zeros too. Squares are summed in fp64,
+ * and f is rounded once, to 24 bits and any exponent, so that rows of any magnitude have it. A row with
+ * an infinity and no NaN has f = 0. Any number of rows.
  *   x, res  T [m][k]; res may be null
  *   gamma   float [k]
  *   res_out T [m][k] output: s; may be null, or x or res itself (in place)

@@ -11,8 +11,8 @@
 // is read once. It also makes q independent of how the row's squares are summed.
 //
 // Bound: memory. A workgroup holds a whole row; 16 lanes hold a 128-block, 8 elements each, and all
-// exchanges are DPP. Squares are summed in fp32 over a lane's 8 elements and in fp64 from there,
-// so neither the row's length nor the order of its waves shows in the fp32 result.
+// exchanges are DPP. Squares are taken and summed in fp64, where those of any fp32 number fit, so that
+// neither the rows' magnitude, nor their length, nor the order of the waves shows in the fp32 result.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -84,14 +84,22 @@ __device__ __forceinline__ double wave_sum(double v)
     return v + __shfl_xor(v, 32);
 }
 
-// r of a row from its waves' sums.
-__device__ __forceinline__ float norm_of(const double *part, int waves, int k, float eps)
+// r of a row from its waves' sums, as up * f: fp32 holds neither 1 / sqrt(mean) of rows of subnormal numbers nor
+// its product with unit of the largest rows with all bits. Multiplied by up first, a power of two, s and amax
+// give what they would with an r of any exponent.
+struct Norm {
+    float f, up;
+};
+__device__ __forceinline__ Norm norm_of(const double *part, int waves, int k, float eps)
 {
     double total = 0.0;
     for (int w = 0; w < waves; ++w)
         total += part[w];
     const double mean = total / (double)k + (double)eps;
-    return mean == 0.0 ? 0.0f : (float)(1.0 / sqrt(mean));   // 0: a row of zeros, eps = 0
+    if (mean == 0.0)   // a row of zeros, eps = 0
+        return {0.0f, 1.0f};
+    const float up = mean < 0x1p-200 ? 0x1p64f : mean > 0x1p200 ? 0x1p-64f : 1.0f;
+    return {(float)(1.0 / sqrt(mean) / (double)up), up};
 }
 
 // Rows of up to 64 blocks: a lane's 8 elements of a row stay in registers until y, those of gamma for
@@ -134,13 +142,13 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
             load(row + gridDim.x);
         if (res_out && on)
             es.store(res_out + i);
-        float sq = 0.0f;
+        double sq = 0.0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sq = fmaf(v[e], v[e], sq);
+            sq = fma((double)v[e], (double)v[e], sq);
             u[e] = v[e] * g[e];
         }
-        const double sum = wave_sum(on ? (double)sq : 0.0);
+        const double sum = wave_sum(on ? sq : 0.0);
         if ((tid & 63) == 0)
             part_s[turn][tid >> 6] = sum;
         rotate_signed(u, lane16);
@@ -153,13 +161,13 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
         __syncthreads();
         if (tid >= 64 && !y)
             continue;
-        const float r = norm_of(part_s[turn], waves, nb * kBlock, eps);
+        const Norm r = norm_of(part_s[turn], waves, nb * kBlock, eps);
         if (tid < nb)   // the first wave's lanes
-            dq[row * nb + tid] = amax_s[turn][tid] * (r * unit);   // r is finite, or the row holds a NaN
+            dq[row * nb + tid] = amax_s[turn][tid] * r.up * (r.f * unit);   // f is finite, or the row holds a NaN
         if (y && on) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = (v[e] * r) * g[e];
+                v[e] = (v[e] * r.up * r.f) * g[e];
             es.set(v);
             es.store(y + i);
         }
@@ -194,13 +202,13 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
             if (res_out)
                 es.store(res_out + i);
             eg.get(g);
-            float sq = 0.0f;
+            double sq = 0.0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sq = fmaf(v[e], v[e], sq);
+                sq = fma((double)v[e], (double)v[e], sq);
                 v[e] *= g[e];
             }
-            sum += (double)sq;
+            sum += sq;
             rotate_signed(v, lane16);
             const float amax = __uint_as_float(amax_bits<4>(v));
             *reinterpret_cast<uint2 *>(q + i) = codes(v, amax, sign);
@@ -211,9 +219,9 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
         if ((tid & 63) == 0)
             part_s[tid >> 6] = sum;
         __syncthreads();
-        const float r = norm_of(part_s, blockDim.x >> 6, nb * kBlock, eps);
+        const Norm r = norm_of(part_s, blockDim.x >> 6, nb * kBlock, eps);
         for (int b = tid; b < nb; b += blockDim.x)
-            dq[row * nb + b] = amax_s[b] * (r * unit);   // r is finite, or the row holds a NaN
+            dq[row * nb + b] = amax_s[b] * r.up * (r.f * unit);   // f is finite, or the row holds a NaN
 
         if (y)
             for (int b = tid >> 4; b < nb; b += groups) {
@@ -230,7 +238,7 @@ __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_long_kernel(
                 eg.get(g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = (v[e] * r) * g[e];
+                    v[e] = (v[e] * r.up * r.f) * g[e];
                 es.set(v);
                 es.store(y + i);
             }

@@ -293,3 +293,52 @@ def test_norm_block_whose_rotation_overflows(k):
     tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 1e-6, None, o.y, o.q, o.dq)
     assert torch.isnan(o.dq[:2, 0]).all() and not o.q[:, :128].any() and o.dq[2, 0] == 0
     assert torch.isfinite(o.dq[:, 1:]).all() and torch.isfinite(o.y).all()
+
+
+@pytest.mark.parametrize("k", [512, 8320])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-120, -90, -70, 58, 70, 90, 110])
+def test_norm_rows_of_any_size(k, dtype, power):
+    """Squares that fp32 cannot hold, eps = 0."""
+    x = (rows(4, k, torch.float32, 32) * 2.0 ** power).to(TYPES[dtype])
+    x[3] = 0
+    gamma = 1 + 0.3 * torch.randn(k, device=gu.DEV)
+    o = Out(4, k, TYPES[dtype])
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 0.0, o.s, o.y, o.q, o.dq)
+    check(x[:3], None, gamma, 0.0, o.s[:3], o.y[:3], o.q[:3], o.dq[:3])
+    assert not o.y[3].any() and not o.q[3].any() and not o.dq[3].any()
+
+
+def test_norm_largest_and_smallest_rows():
+    k = 512
+    x = torch.zeros(3, k, device=gu.DEV)
+    x[0, 7] = 3e38
+    x[1, 300] = -1e-38
+    x[2] = 2.0 ** -148       # f is past the largest fp32
+    gamma = 1 + 0.3 * torch.randn(k, device=gu.DEV)
+    o = Out(3, k, torch.float32)
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 0.0, o.s, o.y, o.q, o.dq)
+    # one element: its normed value is sqrt(k); equal ones: 1. f has 24 bits whatever its exponent: a rounding of f,
+    # two of the products, and one to spare
+    g = gamma.double().cpu().numpy()
+    y = f64(o.y)
+    for row, col, want in ((0, 7, np.sqrt(k) * g[7]), (1, 300, -np.sqrt(k) * g[300])):
+        assert abs(y[row, col] - want) <= 4 * U * abs(want)
+        assert not np.delete(y[row], col).any()
+    assert np.all(np.abs(y[2] - g) <= 4 * U * np.abs(g))
+
+
+@pytest.mark.parametrize("k", [512, 8320])
+def test_norm_scales_of_the_largest_and_smallest_rows(k):
+    x, gamma = torch.zeros(2, k, device=gu.DEV), torch.ones(k, device=gu.DEV)
+    x[0, 7] = 3e38
+    x[1, 300] = 2.0 ** -140
+    gamma[300] = 2.0 ** 100   # the block's amax is 2^-40
+    o = Out(2, k, torch.float32)
+    tb.tb_add_rmsnorm_quant_i8(x, None, gamma, 0.0, None, o.y, o.q, o.dq)
+    # roundings of f, of unit, of their product and of amax times it, and one to spare
+    for row, block, g in ((0, 0, 1.0), (1, 2, 2.0 ** 100)):
+        want = g * np.sqrt(k) / (127 * np.sqrt(128.0))
+        assert abs(float(o.dq[row, block]) - want) <= 5 * U * want
+        assert not np.delete(gu.host(o.dq)[row], block).any()
+        assert (np.abs(gu.host(o.q)[row, 128 * block:128 * (block + 1)]) == 127).all()
