@@ -432,6 +432,8 @@ size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m);
  * Nothing is read back to the host: the lists' lengths stay on the device, and the four calls can
  * be captured in a graph. Each pair's row has the bits that the calls for one matrix give
  * (tb_ffn_gateup_silu, tb_ffn_down on its expert's matrices), however many rows an expert has.
+ * Where a block of h is not finite after its rotation the two differ: here it has qh = 0 and dqh a
+ * NaN, so that the pair's y and its token's sum are NaN too; there a NaN in it is passed over.
  * tokens, topk >= 1; tokens * topk <= 2^31 - 64; experts <= 65536 (else TB_EUNSUPPORTED). */
 typedef struct tb_experts {
     const void *codes;      /* [experts][n][k/128][32] ternary or [...][16] sign */

@@ -234,6 +234,22 @@ struct Core<TB_FMT_SIGN1> {
     }
 };
 
+// rotquant_regs of a block of h held by 16 lanes, but for a block whose rotation is not finite: codes 0
+// and dq a NaN. rotquant_regs' maximum passes over a NaN, and would make a block of zeros of it.
+__device__ __forceinline__ void rotquant_h(float (&v)[8], int lane16, float unit, uint32_t (&packed)[2], float &dq)
+{
+    int qsum;
+    rotquant_regs(v, lane16, unit, packed, dq, qsum);   // v is the rotation now
+    float z = 0.0f;   // 0 times an infinity or a NaN is a NaN
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        z = fmaf(v[e], 0.0f, z);
+    const bool bad = __ballot(z != 0.0f) >> (threadIdx.x & 48) & 0xffff;
+    packed[0] = bad ? 0u : packed[0];
+    packed[1] = bad ? 0u : packed[1];
+    dq = bad ? NAN : dq;
+}
+
 struct MoeArgs {
     const uint8_t *codes[2];
     const uint16_t *scales[2];
@@ -666,8 +682,7 @@ __device__ __forceinline__ void wide_product(const MoeArgs &a, const Tile &tile,
                     v[e] = silu_gate(gp[e], up[e]);
                 uint32_t packed[2];
                 float dq;
-                int qsum;
-                rotquant_regs(v, lane16, a.unit, packed, dq, qsum);
+                rotquant_h(v, lane16, a.unit, packed, dq);
                 const size_t slot = tile.slot + pair;
                 *reinterpret_cast<uint2 *>(a.qh + slot * a.n + n0 + lane16 * 8) = make_uint2(packed[0], packed[1]);
                 if (lane16 == 0)
@@ -898,8 +913,18 @@ __global__ __launch_bounds__(kRotThreads) void moe_rotquant_kernel(const float *
                                                                    int8_t *__restrict__ q, float *__restrict__ dq, float unit)
 {
     const size_t blocks = (size_t)min(max(*used, 0), pairs) * nb, stride = (size_t)gridDim.x * (kRotThreads / 16);
-    for (size_t b = (size_t)blockIdx.x * (kRotThreads / 16) + (threadIdx.x >> 4); b < blocks; b += stride)
-        rotquant16<false>(h + b * kBlock, q + b * kBlock, dq + b, threadIdx.x & 15, unit);
+    const int lane16 = threadIdx.x & 15;
+    for (size_t b = (size_t)blockIdx.x * (kRotThreads / 16) + (threadIdx.x >> 4); b < blocks; b += stride) {
+        float v[8], d;
+        uint32_t packed[2];
+        tbr::Eight<float> h8;
+        h8.load(h + b * kBlock + lane16 * 8);
+        h8.get(v);
+        rotquant_h(v, lane16, unit, packed, d);
+        *reinterpret_cast<uint2 *>(q + b * kBlock + lane16 * 8) = make_uint2(packed[0], packed[1]);
+        if (lane16 == 0)
+            dq[b] = d;
+    }
 }
 
 // out[t] = sum over j, ascending, of weights[t][j] * y[t topk + j], leaving out pairs of no expert.

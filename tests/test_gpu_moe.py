@@ -452,3 +452,43 @@ def test_binding_refusals():
     refuse(tb.Experts, w.gate.codes[:1], w.gate.scales, TERN)
     refuse(tb.Experts, w.gate.codes, w.gate.scales.float(), TERN)
     assert np.isnan(gu.host(r.y)).all() and np.isnan(gu.host(r.h)).all()
+
+
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("t", [7, 90])   # tiles of few and of many pairs
+def test_rows_that_are_not_finite_say_so(fmt, t):
+    """What is not finite in a token's scales is not finite in its sum either."""
+    layer = layer_of(fmt, 3, 640, 384)
+    q, dq = rows(t, 640, 100)
+    ids = ids_of("any", t, 2, 3, 101)
+    dq[1], dq[2, 4], dq[t - 1, 0] = np.nan, np.nan, np.inf
+    run = Run(layer, q, dq, ids).launch()
+    bad = [1, 2, t - 1]
+    assert not torch.isfinite(run.out[bad]).any()
+    offsets, order = plan_of(ids, 3)
+    slots = np.isin(order // 2, bad)
+    assert np.isnan(gu.host(run.dqh)[slots]).all() and not gu.host(run.qh)[slots].any()
+    assert np.isfinite(gu.host(run.dqh)[~slots]).all() and np.isfinite(np.delete(gu.host(run.out), bad, 0)).all()
+
+
+@pytest.mark.parametrize("fmt", [TERN, SIGN])
+@pytest.mark.parametrize("t", [7, 90])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_block_of_h_that_is_not_finite(fmt, t, value):
+    """One value of h that is not finite marks its block of 128, and no other block's bits change."""
+    host = [synth.ffn_layer(102, e, fmt, hidden=640, inter=384) for e in range(3)]
+    gate, up = (tb.Experts.upload([getattr(w, n) for w in host]) for n in ("gate", "up"))
+    q, dq = rows(t, 640, 103)
+    ids = ids_of("any", t, 2, 3, 104)
+    offsets, order = plan_of(ids, 3)
+    out = []
+    for plant in (False, True):
+        if plant:
+            up.scales.view(torch.float16)[1, 128 + 77, 2] = value   # expert 1, column 205: block 1 of h
+        h, qh, dqh = gu.f32_out(2 * t, 384), gu.i8_out(2 * t, 384), gu.f32_out(2 * t, 3)
+        tb.tb_moe_gateup_silu(gate, up, gu.dev(q), gu.dev(dq), 2, gu.dev(offsets), gu.dev(order), h, qh, dqh)
+        out.append((gu.host(qh).reshape(2 * t, 3, 128), gu.host(dqh)))
+    hit = np.zeros((2 * t, 3), bool)
+    hit[offsets[1]:offsets[2], 1] = True
+    assert hit.any() and np.isnan(out[1][1][hit]).all() and not out[1][0][hit].any()
+    assert out[1][0][~hit].tobytes() == out[0][0][~hit].tobytes() and out[1][1][~hit].tobytes() == out[0][1][~hit].tobytes()
