@@ -411,6 +411,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _owned_by(stream, device):
+    """Within it new tensors on `device` belong to `stream`, as the call's stream argument names it: memory
+    that another stream has freed, and may still be using, is not handed to them."""
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)   # None: as it is
+
+
 def tb_add_rmsnorm_quant_i8(x, res, gamma, eps: float, res_out, y, q, dq, stream=None) -> None:
     """s = x + res; q int8 [m][k], dq float32 [m][k/128] = rotated int8 copy of the normed rows.
 
@@ -444,11 +453,13 @@ class Mxfp4:
 
     @classmethod
     def quantise(cls, x, rotate: bool = False, stream=None) -> "Mxfp4":
-        """The rows of x, quantised into new tensors."""
+        """The rows of x, quantised into new tensors, which belong to `stream`: another stream waits for it
+        before it reads them."""
         import torch
         m, k = _matrix_rows("Mxfp4.quantise", "x", x)
-        codes = torch.empty(m, k // 2, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(m, k // 32, dtype=torch.uint8, device=x.device)
+        with _owned_by(stream, x.device):
+            codes = torch.empty(m, k // 2, dtype=torch.uint8, device=x.device)
+            scales = torch.empty(m, k // 32, dtype=torch.uint8, device=x.device)
         tb_mxfp4_quant(x, codes, scales, rotate, stream)
         return cls(codes, scales)
 

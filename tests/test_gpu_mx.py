@@ -265,3 +265,23 @@ def test_binding_refusals():
     refuse(tb.tb_mxfp4_gemm, w, codes.cpu(), scales, y)
     refuse(tb.tb_mxfp4_gemm, w, codes, scales, y.double())
     assert (gu.host(codes) == 0xA5).all() and np.isnan(gu.host(y)).all()
+
+
+def test_quantise_on_another_stream():
+    """The new tensors belong to the stream that writes them: memory that the current stream has freed and
+    may still be using is not handed to another."""
+    n, k = 512, 4096
+    x = torch.randn(n, k, device=gu.DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    freed = [torch.empty(n, w, dtype=torch.uint8, device=gu.DEV) for w in (k // 2, k // 32)]
+    places = {t.data_ptr() for t in freed}
+    del freed
+    for stream in (side, side.cuda_stream):
+        w = tb.Mxfp4.quantise(x, stream=stream)
+        assert w.codes.data_ptr() not in places and w.scales.data_ptr() not in places
+        side.synchronize()
+        want = tb.Mxfp4.quantise(x, stream=torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(w.codes, want.codes) and torch.equal(w.scales, want.scales)
+        del w, want
