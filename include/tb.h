@@ -387,7 +387,7 @@ int tb_add_rmsnorm_quant_i8(const void *x, const void *res, const float *gamma, 
  * e8m0 scale 2^(byte - 127) per 32 elements; byte 255 marks a block that is not a number.
  *   codes  uint8 [rows][k/2]: element i in bits 4 (i % 2) .. + 3 of byte i / 2
  *   scales uint8 [rows][k/32]
- * k is a multiple of 128. Any number of rows. */
+ * k is a multiple of 128. Any number of rows (the product says how many). */
 typedef struct tb_mxfp4 {
     const uint8_t *codes;
     const uint8_t *scales;
@@ -417,10 +417,11 @@ int tb_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int m, int k, 
  *   y  dtype [m][w->n] output
  *   ws workspace of tb_mxfp4_gemm_workspace_bytes(w, m) bytes, 16-byte aligned; null where that
  *      is 0. It needs no initialisation; calls that share one must not overlap in time.
- * m >= 1. TB_EINVAL for a workspace that is too small. */
+ * m >= 1. TB_EINVAL for a workspace that is too small. TB_EUNSUPPORTED unless w->k < 2^24 and
+ * ceil(m / 128) * ceil(w->n / 128) <= 2^23. */
 int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales, int m, void *y,
                   int dtype, void *ws, size_t ws_bytes, void *stream);
-/* Workspace bytes of tb_mxfp4_gemm for m rows (0 also for invalid arguments). */
+/* Workspace bytes of tb_mxfp4_gemm for m rows (0 also for arguments that it refuses). */
 size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m);
 
 /* ---- An FFN of experts --------------------------------------------------

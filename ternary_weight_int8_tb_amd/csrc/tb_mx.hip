@@ -484,7 +484,7 @@ struct MxPlan {
 // 1 x 5120 x 17408 16.5 and 12.8.
 constexpr int kRowsMost = 8, kRowsMostK = 8192;
 constexpr int64_t kRowsMostWeights = 48 << 20;
-int64_t tile_count(int m, int n, int ti, int tj) { return (int64_t)((m + 64 * tj - 1) / (64 * tj)) * ((n + 64 * ti - 1) / (64 * ti)); }
+int64_t tile_count(int64_t m, int64_t n, int ti, int tj) { return (m + 64 * tj - 1) / (64 * tj) * ((n + 64 * ti - 1) / (64 * ti)); }
 MxPlan plan_gemm(int m, int n, int k)
 {
     if (m <= kRowsMost && k <= kRowsMostK && (int64_t)n * k <= kRowsMostWeights)
@@ -561,6 +561,8 @@ size_t code_bytes(int rows, int k) { return (size_t)rows * (k / 2); }
 size_t scale_bytes(int rows, int k) { return (size_t)rows * (k / kMxBlock); }
 
 bool mx_ok(const tb_mxfp4 *w) { return w && w->n >= 1 && w->k >= kBlock && w->k % kBlock == 0; }
+// Lane offsets within a tile's rows, and the tiles of a launch, in 31 bits.
+bool gemm_fits(const tb_mxfp4 *w, int m) { return w->k < 1 << 24 && tile_count(m, w->n, 2, 2) <= 1 << 23; }
 
 }  // namespace
 
@@ -601,7 +603,7 @@ int tb_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int m, int k, 
 
 size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m)
 {
-    if (!mx_ok(w) || m < 1)
+    if (!mx_ok(w) || m < 1 || !gemm_fits(w, m))
         return 0;
     const MxPlan plan = plan_gemm(m, w->n, w->k);
     return plan.parts > 1 ? (size_t)plan.parts * m * w->n * 4 : 0;
@@ -613,8 +615,7 @@ int tb_mxfp4_gemm(const tb_mxfp4 *w, const uint8_t *codes, const uint8_t *scales
     const size_t eb = tbh::dtype_bytes(dtype);
     if (!eb || !mx_ok(w) || m < 1)
         return TB_EINVAL;
-    // lane offsets within a tile's rows, and the tiles of a launch, in 31 bits
-    if ((int64_t)w->k * 128 > 0x7fffffff || (int64_t)((m + 127) / 128) * ((w->n + 127) / 128) > (1 << 23))
+    if (!gemm_fits(w, m))
         return TB_EUNSUPPORTED;
     const size_t need = tb_mxfp4_gemm_workspace_bytes(w, m);
     const tbh::Arg a[] = {{w->codes, code_bytes(w->n, w->k), false},

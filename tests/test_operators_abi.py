@@ -150,6 +150,24 @@ def test_moe_combine(L):
     assert call(tokens=1 << 30, topk=4) == tb.TB_EUNSUPPORTED
 
 
+def test_mx_gemm_limits(L):
+    """Sizes up to the last that an int holds are refused, not counted in 32 bits."""
+    last = 2 ** 31 - 1
+    far = [(i + 1) << 52 for i in range(6)]   # apart, whatever the sizes
+
+    def call(m, n, k):
+        w = tb.CMxfp4(far[0], far[1], n, k)
+        assert L.tb_mxfp4_gemm_workspace_bytes(ctypes.byref(w), m) == 0
+        return L.tb_mxfp4_gemm(ctypes.byref(w), far[2], far[3], m, far[4], 1, far[5], 2 ** 63, None)
+    for m in (last, last - 100, last - 127):
+        assert call(m, 16, 128) == tb.TB_EUNSUPPORTED, m
+        assert call(16, m, 128) == tb.TB_EUNSUPPORTED, m
+    assert call(last, last, 128) == tb.TB_EUNSUPPORTED
+    assert call((1 << 30) + 1, 1, 128) == tb.TB_EUNSUPPORTED   # past 2^23 tiles of 128 x 128
+    assert call(1, 1, 1 << 24) == tb.TB_EUNSUPPORTED
+    assert call(1 << 20, 1 << 20, 128) == tb.TB_EUNSUPPORTED
+
+
 # ---- the tests' own plain implementations -----------------------------------------------
 def test_plain_transform_and_formats():
     rng = np.random.default_rng(5)
