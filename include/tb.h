@@ -435,7 +435,9 @@ size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m);
  * (tb_ffn_gateup_silu, tb_ffn_down on its expert's matrices), however many rows an expert has.
  * Where a block of h is not finite after its rotation the two differ: here it has qh = 0 and dqh a
  * NaN, so that the pair's y and its token's sum are NaN too; there a NaN in it is passed over.
- * tokens, topk >= 1; tokens * topk <= 2^31 - 64; experts <= 65536 (else TB_EUNSUPPORTED). */
+ * tokens, topk >= 1. TB_EUNSUPPORTED unless tokens * topk <= 2^31 - 64, experts <= 65536, an expert's codes
+ * take less than 2 GiB, its lists' tiles times the workgroups of one fit 31 bits, and tb_moe_combine's
+ * n < 2^31 - 1024. */
 typedef struct tb_experts {
     const void *codes;      /* [experts][n][k/128][32] ternary or [...][16] sign */
     const uint16_t *scales; /* [experts][n][k/128], fp16 bits */

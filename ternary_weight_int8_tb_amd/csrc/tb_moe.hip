@@ -1181,7 +1181,8 @@ int tb_moe_combine(const float *y, const float *weights, const int32_t *ids, int
     int rc = check_pairs(tokens, topk);
     if (rc == TB_EINVAL || experts < 1 || n < 1 || !eb)
         return TB_EINVAL;
-    if (rc || experts > kMaxExperts)
+    // the columns of the last workgroup, those past n too, in 31 bits
+    if (rc || experts > kMaxExperts || n > 0x7fffffff - kCombineThreads * 4)
         return TB_EUNSUPPORTED;
     const size_t pairs = (size_t)tokens * topk;
     const tbh::Arg a[] = {{y, pairs * n * 4, false}, {weights, pairs * 4, false}, {ids, pairs * 4, false}, {out, (size_t)tokens * n * eb, true}};

@@ -168,6 +168,13 @@ def test_mx_gemm_limits(L):
     assert call(1 << 20, 1 << 20, 128) == tb.TB_EUNSUPPORTED
 
 
+def test_moe_combine_limits(L):
+    """Columns are counted in 31 bits: the last workgroup's have to fit too."""
+    far = [(i + 1) << 52 for i in range(4)]
+    for n in (2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 - 1023):
+        assert L.tb_moe_combine(far[0], far[1], far[2], 1, 1, 4, n, far[3], 1, None) == tb.TB_EUNSUPPORTED, n
+
+
 # ---- the tests' own plain implementations -----------------------------------------------
 def test_plain_transform_and_formats():
     rng = np.random.default_rng(5)
