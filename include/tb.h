@@ -437,7 +437,9 @@ size_t tb_mxfp4_gemm_workspace_bytes(const tb_mxfp4 *w, int m);
  * NaN, so that the pair's y and its token's sum are NaN too; there a NaN in it is passed over.
  * tokens, topk >= 1. TB_EUNSUPPORTED unless tokens * topk <= 2^31 - 64, experts <= 65536, an expert's codes
  * take less than 2 GiB, its lists' tiles times the workgroups of one fit 31 bits, and tb_moe_combine's
- * n < 2^31 - 1024. */
+ * n < 2^31 - 1024.
+ * scales are read by whole words of 4 bytes: where experts * n * k / 128 is odd, the last one ends 2 bytes
+ * behind the array (nothing depends on them). */
 typedef struct tb_experts {
     const void *codes;      /* [experts][n][k/128][32] ternary or [...][16] sign */
     const uint16_t *scales; /* [experts][n][k/128], fp16 bits */
