@@ -261,8 +261,9 @@ def tb_sign_interleave(w: Matrix, stream=None) -> Matrix:
     """The TB_FMT_SIGN1_RI4 copy of a sign matrix (rows interleaved by four), in new device
     tensors, for the lookup-table GEMV."""
     import torch
-    codes = torch.empty_like(w.codes)
-    scales = torch.empty_like(w.scales)
+    with _owned_by(stream, w.codes.device):
+        codes = torch.empty_like(w.codes)
+        scales = torch.empty_like(w.scales)
     _call("tb_sign_interleave", ctypes.byref(w.c), codes.data_ptr(), scales.data_ptr(),
           _stream(stream))
     return Matrix(codes, scales, w.n, w.k, TB_FMT_SIGN1_RI4)

@@ -117,3 +117,19 @@ def test_lut_limits():
     with pytest.raises(tb.TbError) as e:
         tb.tb_ffn_gateup_silu(ri, ri, q[:1], dq[:1], h)
     assert e.value.status == tb.TB_EUNSUPPORTED
+
+
+def test_interleave_on_another_stream():
+    """The new tensors are not memory that the current stream has freed and may still be using."""
+    w = tb.Matrix.upload(synth.matrix(SIGN, 1024, 2048, 77, 0, synth.T_DOWN))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    freed = [torch.empty_like(w.codes), torch.empty_like(w.scales)]
+    places = {t.data_ptr() for t in freed}
+    del freed
+    r = tb.tb_sign_interleave(w, stream=side)
+    assert r.codes.data_ptr() not in places and r.scales.data_ptr() not in places
+    side.synchronize()
+    want = tb.tb_sign_interleave(w)
+    assert torch.equal(r.codes, want.codes) and torch.equal(r.scales, want.scales)
