@@ -285,3 +285,13 @@ def test_quantise_on_another_stream():
         want = tb.Mxfp4.quantise(x, stream=torch.cuda.current_stream().cuda_stream)
         assert torch.equal(w.codes, want.codes) and torch.equal(w.scales, want.scales)
         del w, want
+
+
+# the row kernel with each number of rows, past 16 weight rows and past whole 256 elements of k, and the first
+# that goes in tiles
+@pytest.mark.parametrize("m,n,k", [(4, 100, 640), (5, 1000, 8064), (6, 33, 2432), (7, 250, 896), (8, 17, 384), (8, 9216, 5120), (8, 31, 8192),
+                                   (8, 250, 896), (9, 250, 896), (8, 40, 8320)])
+def test_gemm_few_rows(m, n, k):
+    test_gemm_exact(m, n, k)
+    for dtype in TYPES:
+        test_gemm(m, n, k, dtype)
