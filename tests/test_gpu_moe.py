@@ -492,3 +492,24 @@ def test_block_of_h_that_is_not_finite(fmt, t, value):
     hit[offsets[1]:offsets[2], 1] = True
     assert hit.any() and np.isnan(out[1][1][hit]).all() and not out[1][0][hit].any()
     assert out[1][0][~hit].tobytes() == out[0][0][~hit].tobytes() and out[1][1][~hit].tobytes() == out[0][1][~hit].tobytes()
+
+
+@pytest.mark.parametrize("t", [9, 90])
+def test_offsets_that_are_no_plan_write_inside_the_outputs(t):
+    """The outputs lie between poisoned rows of larger arrays, which stay as they are."""
+    layer = layer_of(TERN, 3, 640, 384)
+    q, dq = rows(t, 640, 105)
+    p, pad = 2 * t, 16
+    for bad in ([0, 2 * t, 0, 2 * t], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 2 ** 31 - 1], [5, 5, 5, 5], [-5, 7, 4, 1000]):
+        offsets = gu.dev(np.array(bad, np.int32))
+        order = gu.dev(np.random.default_rng(106).integers(-p, 2 * p, p).astype(np.int32))
+        whole = {"h": gu.f32_out(p + 2 * pad, 384), "qh": gu.i8_out(p + 2 * pad, 384), "dqh": gu.f32_out((p + 2 * pad) * 4, 3),
+                 "y": gu.f32_out(p + 2 * pad, 640)}
+        part = {n: a[pad:pad + p] for n, a in whole.items()}
+        part["dqh"] = whole["dqh"][4 * pad:4 * pad + p]
+        tb.tb_moe_gateup_silu(layer.gate, layer.up, gu.dev(q), gu.dev(dq), 2, offsets, order, part["h"], part["qh"], part["dqh"])
+        tb.tb_moe_down(layer.down, part["qh"], part["dqh"], offsets, order, part["y"])
+        for n, a in whole.items():
+            lo = 4 * pad if n == "dqh" else pad
+            for around in (a[:lo], a[lo + p:]):
+                assert (gu.host(around) == gu.POISON_I8).all() if n == "qh" else np.isnan(gu.host(around)).all(), (n, bad)
