@@ -515,10 +515,13 @@ struct StepRow {
 // last half phase of a step is multiplied.
 // Bound: vector operations, 34 for a 16x16 tile of one block: 16 of the fold (a difference, two
 // products, a sum, for 4 values), 6 of the decode, shared by 48 pairs, 8 of SiLU and rotation. 32768
-// pairs over 64 experts, ternary, 2 x 1024 x 2048: 314 us, 143 M of them, one every 4.3 cycles of a SIMD;
-// down 198 us.
+// pairs over 64 experts, ternary, 2 x 1024 x 2048: 314 to 340 us by the card, 143 M of them, one every 4.3 cycles of a SIMD;
+// down 198 to 209 us. Sign: 369 to 378 and 320 to 327 us.
 // 16 waves per CU, because a wave alone issues a vector operation every 5 to 6 cycles and four of a
-// SIMD together one every 2.3.
+// SIMD together one every 2.3. The 128 registers that this leaves a wave do not hold everything: 15
+// (ternary) and 47 (sign) of gate/up and 4 and 30 of down lie in scratch memory. Ternary reads them back
+// outside the loop over the steps but for one; sign reads 28 and 24 within its three loops (of 1, 2 and 3 groups of
+// pairs), which is part of why it is slower, by how much is not known.
 // ------------------------------------------------------------------------------------
 template <int FMT, bool TWO>
 struct WideShape {

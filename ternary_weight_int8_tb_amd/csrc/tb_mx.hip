@@ -99,7 +99,8 @@ __global__ __launch_bounds__(kQuantThreads) void mx_dequant_kernel(const uint32_
 // the weights, B the activation, so an operand of either comes from its row, with no exchange and no
 // LDS. k goes in halves of 256 elements, a 128-byte line of codes; lane group g takes blocks 2 g and
 // 2 g + 1 of a half, whose two scales are one 16-bit load.
-// A workgroup owns 16 weight rows and all (up to 16) activation rows; its waves split k, and add their
+// A workgroup owns 16 weight rows and all activation rows (the plan gives it up to kRowsMost, the operand
+// holds 16); its waves split k, and add their
 // sums through LDS in wave order: the order depends on k alone. Bound: the weights' way from
 // memory; a wave has the loads of U halves in flight at a time.
 // ------------------------------------------------------------------------------------
@@ -206,8 +207,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void mx_rows_kernel(const uint8_t *
 //     LDS cycle serves read 16 different columns of banks. A group's scales go the same way.
 // Bound: matrix rate. Per 64 elements of k a wave's TI TJ instructions take 32 TI TJ cycles and TI + TJ
 // reads of 1 KB: at 4 x 4 all four waves read 64 bytes a cycle of the 128 that LDS gives. Measured:
-// 8192 x 17408 x 5120 430 to 480 us, 3.0 to 3.4 PFLOP/s; the instruction alone, on random codes, runs at
-// 6.6 to 7.5 (9.9 on zeros: power bounds it).
+// 8192 x 17408 x 5120 430 to 500 us by the card, 2.9 to 3.4 PFLOP/s; the instruction alone, on random codes, runs at
+// 6.6 to 7.5 (9.9 on zeros: power bounds it). 4 x 4 leaves one wave a SIMD, which stands at every barrier.
 // ------------------------------------------------------------------------------------
 constexpr int kGroup = 512;              // elements of k whose scales are loaded together
 constexpr uint32_t kBufWord3 = 0x00020000u;
@@ -478,9 +479,10 @@ struct MxPlan {
     int ti, tj, parts;
 };
 // Up to 8 rows of up to 8192 elements, and 2^20 x 48 weights: one launch of the row kernel; the tiles, which
-// stream the weights through LDS in whole lines, need a second launch for the sums. Measured, us a call,
-// row kernel and tiles: 1 x 5120 x 4096 6.6 and 9.8, 1 x 9216 x 5120 8.8 and 9.5, 8 x 9216 x 5120 10.5 and
-// 10.0, 16 x 9216 x 5120 12.2 and 10.2, 1 x 17408 x 5120 13.7 and 13.2, 8 x 17408 x 5120 16.3 and 13.6,
+// stream the weights through LDS in whole lines, need a second launch for the sums, and a workspace. us a
+// call in a captured graph, row kernel and tiles: 1 x 5120 x 4096 5.6 and 7.8, 1 x 9216 x 5120 9.3 and 9.8,
+// 8 x 9216 x 5120 10.8 and 10.2 (what the rule gives away for one rule up to 8 rows). Beyond it, enqueued
+// one by one: 16 x 9216 x 5120 12.2 and 10.2, 1 x 17408 x 5120 13.7 and 13.2, 8 x 17408 x 5120 16.3 and 13.6,
 // 1 x 5120 x 17408 16.5 and 12.8.
 constexpr int kRowsMost = 8, kRowsMostK = 8192;
 constexpr int64_t kRowsMostWeights = 48 << 20;
@@ -489,12 +491,14 @@ MxPlan plan_gemm(int m, int n, int k)
 {
     if (m <= kRowsMost && k <= kRowsMostK && (int64_t)n * k <= kRowsMostWeights)
         return {0, 0, 1};
+    // By the tiles alone, whatever m is: few rows of a very wide layer multiply rows that are not there. 1, 8 and
+    // 64 x 160000 x 5120 take 136, 136 and 149 us, where reading the weights would take 74.
     if (tile_count(m, n, 4, 4) >= 192)
         return {4, 4, 1};
-    // 128 x 64 tiles while they are few; k in parts until there are two workgroups for each CU, or one
-    // where the parts' sums are many (24 x 5120 x 17408: 15.1 us in 6 parts, 14.3 in 12;
-    // 256 x 5120 x 5120: 17.2 in 3, 16.7 in 1; 509 x 5120 x 4096: 21.6 as 128 x 128 in 3 parts, 16.3 as
-    // 128 x 64 in 1; 512 x 9216 x 5120: 25.4 as 128 x 128 and 27.9 as 128 x 64)
+    // 128 x 64 tiles while they are few; k in parts until there are two workgroups for each of the chip's 256
+    // CUs, or one where the parts' sums are many. us a call in a captured graph: 24 x 5120 x 17408 15.3 in 6 parts,
+    // 14.7 in 12; 256 x 5120 x 5120 17.4 in 3, 17.0 in 1; 509 x 5120 x 4096 17.0 as 128 x 128 and 16.7 as 128 x 64;
+    // 512 x 9216 x 5120 25.4 as 128 x 128 and 27.7 as 128 x 64.
     const int tj = tile_count(m, n, 2, 1) <= 512 ? 1 : 2, groups = (k + kGroup - 1) / kGroup;
     const int64_t tiles = tile_count(m, n, 2, tj), most = m <= 64 ? 512 : 256;
     return {2, tj, (int)std::min<int64_t>(std::max<int64_t>(1, most / tiles), std::max(1, groups / 2))};

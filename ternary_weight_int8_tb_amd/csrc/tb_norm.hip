@@ -105,7 +105,7 @@ __device__ __forceinline__ Norm norm_of(const double *part, int waves, int k, fl
 // Rows of up to 64 blocks: a lane's 8 elements of a row stay in registers until y, those of gamma for
 // all rows of the workgroup, and the next row's are on their way while this one's norm is
 // summed (8192 rows of 5120 bf16 with res: 85 us with a row per workgroup, which waits for its loads and
-// then for its sum; 55 us so).
+// then for its sum; 56 us so).
 // LDS is used in turn by odd and even rows, so that one barrier per row is enough.
 template <class T>
 __global__ __launch_bounds__(kMaxThreads) void add_rmsnorm_quant_kernel(
