@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define TB_ABI_VERSION 7
+#define TB_ABI_VERSION 8
 #define TB_BLOCK 128
 #define TB_MAX_ROWS 8
 #define TB_MAX_BATCH_ROWS 32
@@ -483,6 +483,121 @@ int tb_moe_down(const tb_experts *wd, const int8_t *qh, const float *dqh, int pa
  *   out dtype [tokens][n] output */
 int tb_moe_combine(const float *y, const float *weights, const int32_t *ids, int tokens, int topk,
                    int experts, int n, void *out, int dtype, void *stream);
+
+/* ---- Attention over a paged cache -----------------------------------------
+ * What a full-attention layer does between its two projections. Keys and values lie in pages of a
+ * fixed number of tokens; a block table names each request's pages in order.
+ *   tb_kv_plan, once a step -> tb_rope_kv and tb_attn_paged, in every layer
+ * Lengths stay on the device, so that the calls can be captured in a graph and replayed while the
+ * requests grow.
+ * Caches: every page of a kv head is contiguous, [pages][kv_heads][page][dim] for k and for v, in
+ * bf16 or fp16. page is 16, 32, 64, 128 or 256. A page id outside [0, pages) names no page: nothing
+ * is written there, and its keys are left out. pages * page < 2^31. */
+typedef struct tb_kv_cache {
+    void *k;
+    void *v;
+    int32_t pages;
+    int32_t kv_heads;
+    int32_t page;  /* tokens of a page */
+    int32_t dim;   /* elements of a head: a multiple of 16, up to 512 */
+    int32_t dtype; /* TB_BF16 or TB_F16 */
+} tb_kv_cache;
+
+/* Rows of heads within wider rows (a fused projection's): head h of row t is the dim consecutive elements
+ * from data + t * row_stride + h * head_stride on. Strides count elements, are multiples of 8 and not
+ * negative; that of a single row or a single head is not read. data is 16-byte aligned. */
+typedef struct tb_heads {
+    const void *data;
+    int64_t row_stride;
+    int64_t head_stride;
+    int32_t heads;
+    int32_t dtype;
+} tb_heads;
+
+/* Block tables and slots of a step, from the requests' lengths. In this order:
+ *   - a request with fresh[s] < 0 has ended: the pages of its context are pushed on the free list (in
+ *     the order of its table; entries that name no page are passed over), and its length is 0. Its
+ *     table row is left as it was;
+ *   - the others get fresh[s] rows of the step, one after another, as far as `rows` go:
+ *       offsets[s + 1] = min(rows, sum of fresh[0 .. s]), lengths[s] = context[s] + its rows;
+ *   - pages that a request's length needs beyond those of its context are popped from the end of the free
+ *     list, request by request, page by page, into its table row. Where the list is empty, the entry is -1;
+ *   - row t, the i-th of request s: positions[t] = context[s] + i, and slots[t] = page id * page + place in
+ *     the page, or -1 where the position has no page. Rows behind the last request's have -1 in both.
+ *   context   int32 [requests]: tokens that the cache holds (negative counts as 0)
+ *   fresh     int32 [requests]: new tokens of the step; 0 for a request that waits
+ *   table     int32 [requests][width], updated
+ *   free_list int32 [pages], updated; count int32 [1]: its entries. Entries from left[0] on are
+ *             unspecified
+ *   lengths   int32 [requests] output; may be context itself
+ *   offsets   int32 [requests + 1], positions, slots int32 [rows] outputs
+ *   left      int32 [1] output: entries of the free list afterwards; may be count itself
+ *   missing   int32 [1] output: rows of requests that have no slot (0 unless pages or width ran out)
+ * requests, rows, width >= 1. TB_EUNSUPPORTED unless requests <= 16384, rows < 2^30,
+ * requests * width < 2^30 and width * page <= 2^30; a context longer than 2^30 counts as that. */
+int tb_kv_plan(const int32_t *context, const int32_t *fresh, int requests, int rows, int page, int pages,
+               int32_t *table, int width, int32_t *free_list, const int32_t *count, int32_t *lengths,
+               int32_t *offsets, int32_t *positions, int32_t *slots, int32_t *left, int32_t *missing,
+               void *stream);
+
+enum tb_rope_layout {
+    TB_ROPE_HALF = 0,       /* pair i: elements i and rot / 2 + i */
+    TB_ROPE_INTERLEAVED = 1 /* pair i: elements 2 i and 2 i + 1 */
+};
+/* Rotary positions: pair i of a row at position p is turned by p * freq[i] and multiplied by factor. Scalings
+ * for long contexts are a choice of freq and factor (the binding's Rope.frequencies makes them). */
+typedef struct tb_rope {
+    const double *freq; /* device, [rot / 2], radians per position */
+    int32_t rot;        /* elements that are turned, from a head's first on: a multiple of 16, up to dim */
+    int32_t layout;
+    float factor;
+} tb_rope;
+
+/* Rotate the rows of q into q_out, and those of k into the cache, and copy those of v there:
+ *   (a, b) -> (a c - b s, b c + a s), c = factor * cos(p freq), s = factor * sin(p freq)
+ * in fp32 (the angle in fp64: far positions keep it), rounded once to the output's type. Elements from rot
+ * on are copied.
+ *   q, k, v   rows [tokens][heads][dim] of one type, any of tb_dtype; k and v with cache->kv_heads heads.
+ *             q (with q_out), or k, v, slots and cache, may be null; dim is the cache's, if there is one
+ *   rope      null: nothing is turned
+ *   positions int32 [tokens]; a row with a negative one is padding: nothing is done for it
+ *   slots     int32 [tokens], from tb_kv_plan; one outside [0, pages * page) is not written. Two rows
+ *             with one slot leave either's values
+ *   q_out     dtype [tokens][q->heads][dim] output
+ * tokens >= 1. TB_EUNSUPPORTED unless tokens < 2^24. */
+int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int tokens, int dim, const tb_rope *rope,
+               const int32_t *positions, const int32_t *slots, const tb_kv_cache *cache, void *q_out, int dtype,
+               void *stream);
+
+/* Attention of each request's newest tokens over its pages. Request s has the rows
+ * offsets[s] .. offsets[s + 1] - 1 of q, the last ones of its lengths[s] tokens. With p the position of such
+ * a row's token, it sees the keys j <= p, of these with a window only j > p - window:
+ *   o = sum_j softmax_j(scale * q . k_j) v_j      out = o / (1 + exp(-gate))  (without a gate: o)
+ * Head h of q reads kv head h / (q->heads / kv_heads). Sums and softmax are held in fp32. Keys whose page id
+ * names no page, or whose page lies beyond the table, are left out. A row that sees no key has o = 0. What
+ * a row does not see cannot reach it, be it a NaN; where it sees a value that is not finite, its result is infinite
+ * or NaN. A row whose scores are all -infinity has o = 0.
+ * Products run on the matrix instructions of the cache's type. q of that type enters them as it is, and the
+ * weights of the softmax are rounded to it; of fp32 rows q and the weights are split into parts whose sum has
+ * 22 bits (fp16) or 24 (bf16).
+ * The order of the sums, and so a row's low-order bits, depend on the lengths of all requests of the call;
+ * the same call gives the same bits.
+ *   q         [tokens][heads][dim], fp32 or the cache's type; dim 64, 128 or 256
+ *   gate      null, or rows like q's, of any type
+ *   table     int32 [requests][width]
+ *   offsets   int32 [requests + 1], from 0 on, not descending; lengths int32 [requests]
+ *   window    0: none
+ *   out       q's type [tokens][heads][dim] output; rows of no request are left as they were
+ *   ws        workspace of tb_attn_paged_workspace_bytes bytes, 16-byte aligned; no initialisation. Calls
+ *             that share one must not overlap in time
+ * scale > 0 and finite, heads a multiple of kv_heads, requests, tokens, width >= 1, window >= 0.
+ * TB_EUNSUPPORTED unless dim is one of those above, requests <= 65536, tokens * heads < 2^30,
+ * width * page <= 2^30 and (tokens * heads / 16 + requests * kv_heads) * (width * page / 64 + 2) < 2^31. */
+int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,
+                  const int32_t *offsets, const int32_t *lengths, int requests, int tokens, float scale, int window,
+                  void *out, void *ws, size_t ws_bytes, void *stream);
+/* Workspace bytes for q rows of `dtype` (0 for arguments that the call refuses). */
+size_t tb_attn_paged_workspace_bytes(const tb_kv_cache *cache, int heads, int dtype, int requests, int tokens);
 
 /* Static description of a status code; never NULL. */
 const char *tb_status_str(int status);

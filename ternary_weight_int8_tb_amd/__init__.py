@@ -23,8 +23,9 @@ TB_FMT_TERNARY2, TB_FMT_SIGN1, TB_FMT_SIGN1_RI4 = 0, 1, 2
 BLOCK = 128
 MAX_ROWS = 8
 MAX_BATCH_ROWS = 32
-ABI_VERSION = 7
+ABI_VERSION = 8
 TB_F32, TB_BF16, TB_F16 = 0, 1, 2
+TB_ROPE_HALF, TB_ROPE_INTERLEAVED = 0, 1
 
 # every symbol include/tb.h declares
 ABI_SYMBOLS = ("tb_rotate_quant_i8", "tb_gemv_ternary", "tb_gemv_ternary_x", "tb_ffn_gateup_silu",
@@ -40,6 +41,7 @@ ABI_SYMBOLS = ("tb_rotate_quant_i8", "tb_gemv_ternary", "tb_gemv_ternary_x", "tb
                "tb_add_rmsnorm_quant_i8",
                "tb_mxfp4_quant", "tb_mxfp4_dequant", "tb_mxfp4_gemm", "tb_mxfp4_gemm_workspace_bytes",
                "tb_moe_plan", "tb_moe_gateup_silu", "tb_moe_down", "tb_moe_combine",
+               "tb_kv_plan", "tb_rope_kv", "tb_attn_paged", "tb_attn_paged_workspace_bytes",
                "tb_status_str", "tb_abi_version")
 TB_FFN_CHAIN = 1
 
@@ -69,11 +71,28 @@ class CExperts(ctypes.Structure):
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
+class CKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class CHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _XP = ctypes.POINTER(CMxfp4)
 _EP = ctypes.POINTER(CExperts)
 _MP = ctypes.POINTER(CMatrix)
+_CP = ctypes.POINTER(CKvCache)
+_HP = ctypes.POINTER(CHeads)
+_RP = ctypes.POINTER(CRope)
 _SIGS = {
     "tb_rotate_quant_i8": ([_P, _I, _I, _P, _P, _P], _I),
     "tb_gemv_ternary": ([_MP, _P, _P, _I, _P, _P], _I),
@@ -107,6 +126,10 @@ _SIGS = {
     "tb_moe_gateup_silu": ([_EP, _EP, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P], _I),
     "tb_moe_down": ([_EP, _P, _P, _I, _P, _P, _P, _P], _I),
     "tb_moe_combine": ([_P, _P, _P, _I, _I, _I, _I, _P, _I, _P], _I),
+    "tb_kv_plan": ([_P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "tb_rope_kv": ([_HP, _HP, _HP, _I, _I, _RP, _P, _P, _CP, _P, _I, _P], _I),
+    "tb_attn_paged": ([_HP, _HP, _CP, _P, _I, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, ctypes.c_size_t, _P], _I),
+    "tb_attn_paged_workspace_bytes": ([_CP, _I, _I, _I, _I], ctypes.c_size_t),
     "tb_status_str": ([_I], ctypes.c_char_p),
     "tb_abi_version": ([], _I),
 }
@@ -590,3 +613,157 @@ def tb_moe_combine(y, weights, ids, experts: int, out, stream=None) -> None:
     _check(fn, dev, ("y", y, torch.float32, (t * topk, n)), ("weights", weights, torch.float32, (t, topk)),
            ("ids", ids, torch.int32, (t, topk)), ("out", out, out.dtype, (t, n)))
     _launch(fn, dev, stream, y.data_ptr(), weights.data_ptr(), ids.data_ptr(), t, topk, experts, n, out.data_ptr(), code)
+
+
+# ---- attention over a paged cache ---------------------------------------------------------
+class KvCache:
+    """A paged cache of one layer: k, v bfloat16 or float16 [pages][kv_heads][page][dim]; page is 16, 32, 64, 128 or 256."""
+
+    def __init__(self, k, v):
+        fn = "KvCache"
+        if k.dim() != 4 or not k.is_cuda or not k.is_contiguous() or k.dtype not in (_torch().bfloat16, _torch().float16):
+            _bad(fn, "k has to be a contiguous bfloat16 or float16 tensor [pages][kv_heads][page][dim] on the GPU")
+        _check(fn, k.device, ("v", v, k.dtype, k.shape))
+        self.k, self.v, self.device = k, v, k.device
+        self.pages, self.kv_heads, self.page, self.dim = (int(n) for n in k.shape)
+        self.dtype = _dtype(fn, k)
+        self.c = CKvCache(k.data_ptr(), v.data_ptr(), self.pages, self.kv_heads, self.page, self.dim, self.dtype)
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """Rotary positions: freq float64 [rot/2], radians per position of each pair, on the GPU; layout TB_ROPE_HALF or
+    TB_ROPE_INTERLEAVED; factor multiplies what is turned."""
+
+    def __init__(self, freq, layout: int = TB_ROPE_HALF, factor: float = 1.0):
+        fn = "Rope"
+        if freq.dim() != 1 or not freq.is_cuda:
+            _bad(fn, "freq has to be a float64 vector on the GPU")
+        _check(fn, freq.device, ("freq", freq, _torch().float64, freq.shape))
+        self.freq, self.device, self.rot, self.layout, self.factor = freq, freq.device, 2 * int(freq.shape[0]), int(layout), float(factor)
+        self.c = CRope(freq.data_ptr(), self.rot, self.layout, self.factor)
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def frequencies(rot: int, base: float = 10000.0, scaling: str = "none", stretch: float = 1.0, trained: float = 0.0,
+                    slow: float = 1.0, fast: float = 32.0):
+        """(freq float64 [rot/2] on the CPU, factor) of base^(-2i/rot), scaled for contexts `stretch` times as long as the
+        trained length:
+
+        "none"    not at all
+        "linear"  every pair is slowed by stretch
+        "base"    the base is raised, so that the slowest pair is slowed by stretch and the fastest is kept
+        "parts"   pairs that turn less than `slow` times over the trained length are slowed by stretch, those that turn more
+                  than `fast` times are kept, those between are mixed in proportion; factor = 0.1 ln(stretch) + 1"""
+        import math
+        import torch
+        fn = "Rope.frequencies"
+        if rot < 2 or rot % 2 or not base > 0 or not stretch > 0:
+            _bad(fn, f"rot {rot}, base {base}, stretch {stretch}")
+        if scaling == "base":
+            base *= stretch ** (rot / (rot - 2)) if rot > 2 else 1.0
+        f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+        if scaling in ("none", "base"):
+            return f, 1.0
+        if scaling == "linear":
+            return f / stretch, 1.0
+        if scaling != "parts" or not trained > 0 or not fast > slow:
+            _bad(fn, f"scaling {scaling!r}, trained {trained}, slow {slow}, fast {fast}")
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        return f * (keep + (1 - keep) / stretch), 0.1 * math.log(stretch) + 1 if stretch > 1 else 1.0
+
+    @classmethod
+    def make(cls, rot: int, layout: int = TB_ROPE_HALF, device="cuda", **scaling) -> "Rope":
+        """frequencies(rot, **scaling) on the device."""
+        freq, factor = cls.frequencies(rot, **scaling)
+        return cls(freq.to(device), layout, factor)
+
+
+def _heads(fn: str, name: str, t, device, rows: int, dim: int):
+    """A view [rows][heads][dim] of wider rows as a tb_heads."""
+    if t.dim() != 3 or not t.is_cuda or t.device != device or t.shape[0] != rows or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+        _bad(fn, f"{name} has to be a tensor [{rows}][heads][{dim}] on {device} with consecutive elements of a head")
+    return CHeads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], _dtype(fn, t))
+
+
+def tb_kv_plan(context, fresh, page: int, pages: int, table, free_list, count, lengths, offsets, positions, slots, left, missing,
+               stream=None) -> None:
+    """Block tables and slots of a step (int32 tensors).
+
+    context, fresh [requests] (fresh -1: the request has ended), table [requests][width] and free_list [pages] updated,
+    count [1] -> lengths [requests] (may be context), offsets [requests + 1], positions, slots [rows], left [1] (may be
+    count), missing [1]."""
+    fn = "tb_kv_plan"
+    n, width = _matrix_rows(fn, "table", table)
+    dev, i32 = table.device, _torch().int32
+    if positions.dim() != 1:
+        _bad(fn, "positions has to be a vector")
+    rows = positions.shape[0]
+    _check(fn, dev, ("table", table, i32, (n, width)), ("context", context, i32, (n,)), ("fresh", fresh, i32, (n,)),
+           ("free_list", free_list, i32, (pages,)), ("count", count, i32, (1,)), ("lengths", lengths, i32, (n,)),
+           ("offsets", offsets, i32, (n + 1,)), ("positions", positions, i32, (rows,)), ("slots", slots, i32, (rows,)),
+           ("left", left, i32, (1,)), ("missing", missing, i32, (1,)))
+    _launch(fn, dev, stream, context.data_ptr(), fresh.data_ptr(), n, rows, page, pages, table.data_ptr(), width, free_list.data_ptr(),
+            count.data_ptr(), lengths.data_ptr(), offsets.data_ptr(), positions.data_ptr(), slots.data_ptr(), left.data_ptr(),
+            missing.data_ptr())
+
+
+def tb_rope_kv(q, k, v, rope: Rope | None, positions, slots, cache: KvCache | None, q_out, stream=None) -> None:
+    """q_out [tokens][heads][dim] = the rotated rows of q; those of k, and v as they are, into the cache's slots.
+
+    q, k, v [tokens][heads][dim] of one type (float32, bfloat16, float16), views of wider rows as they come; positions,
+    slots int32 [tokens] from tb_kv_plan. q and q_out, or k, v, slots and cache, may be None; rope None: nothing is turned."""
+    fn = "tb_rope_kv"
+    x = q if q is not None else k
+    if x is None or x.dim() != 3 or (q is None) != (q_out is None):
+        _bad(fn, "q has to be a tensor [tokens][heads][dim], with q_out, or None in both places")
+    dev, i32 = x.device, _torch().int32
+    t, dim = x.shape[0], x.shape[2]
+    _check(fn, dev, ("positions", positions, i32, (t,)))
+    hq = hk = hv = None
+    code = 0
+    if q is not None:
+        hq, code = ctypes.byref(_heads(fn, "q", q, dev, t, dim)), _dtype(fn, q_out)
+        _check(fn, dev, ("q_out", q_out, q_out.dtype, q.shape))
+    if k is not None or v is not None or slots is not None or cache is not None:
+        if k is None or v is None or slots is None or cache is None:
+            _bad(fn, "k, v, slots and cache come together")
+        if cache.device != dev:
+            _bad(fn, f"the cache is on {cache.device}, the rows on {dev}")
+        hk, hv = ctypes.byref(_heads(fn, "k", k, dev, t, dim)), ctypes.byref(_heads(fn, "v", v, dev, t, dim))
+        _check(fn, dev, ("slots", slots, i32, (t,)))
+    if rope is not None and rope.device != dev:
+        _bad(fn, f"freq is on {rope.device}, the rows on {dev}")
+    _launch(fn, dev, stream, hq, hk, hv, t, dim, None if rope is None else rope.ref, positions.data_ptr(), _ptr(slots),
+            None if cache is None else cache.ref, _ptr(q_out), code)
+
+
+def tb_attn_paged_workspace_bytes(cache: KvCache, heads: int, dtype, requests: int, tokens: int) -> int:
+    """Bytes of device workspace tb_attn_paged needs for q rows of a torch dtype."""
+    torch = _torch()
+    code = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.float16: TB_F16}.get(dtype, -1)
+    return int(lib().tb_attn_paged_workspace_bytes(cache.ref, int(heads), code, int(requests), int(tokens)))
+
+
+def tb_attn_paged(q, cache: KvCache, table, offsets, lengths, scale: float, out, ws, gate=None, window: int = 0, stream=None) -> None:
+    """out [tokens][heads][dim] = attention of each request's rows (offsets[s] .. offsets[s+1] - 1, the last of its lengths[s]
+    tokens) over its pages, times sigmoid(gate).
+
+    q [tokens][heads][dim], float32 or the cache's type (a view of wider rows as it comes), and gate alike, of any type; table
+    int32 [requests][width], offsets int32 [requests + 1], lengths int32 [requests]; ws a uint8 workspace of
+    tb_attn_paged_workspace_bytes bytes."""
+    torch = _torch()
+    fn = "tb_attn_paged"
+    n, width = _matrix_rows(fn, "table", table)
+    if q.dim() != 3:
+        _bad(fn, "q has to be a tensor [tokens][heads][dim]")
+    dev, i32, dim = cache.device, torch.int32, cache.dim
+    t, heads = q.shape[0], q.shape[1]
+    _check(fn, dev, ("table", table, i32, (n, width)), ("offsets", offsets, i32, (n + 1,)), ("lengths", lengths, i32, (n,)),
+           ("out", out, q.dtype, (t, heads, dim)), ("ws", ws, torch.uint8, (ws.numel(),)))
+    hq = _heads(fn, "q", q, dev, t, dim)
+    hg = None
+    if gate is not None:
+        hg = ctypes.byref(_heads(fn, "gate", gate, dev, t, dim))
+    _launch(fn, dev, stream, ctypes.byref(hq), hg, cache.ref, table.data_ptr(), width, offsets.data_ptr(), lengths.data_ptr(), n, t, scale,
+            window, out.data_ptr(), ws.data_ptr(), ws.numel())

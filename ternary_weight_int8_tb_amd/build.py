@@ -9,7 +9,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = ("tb.hip", "tb_norm.hip", "tb_mx.hip", "tb_moe.hip")   # libtb.so, one object each
+SOURCES = ("tb.hip", "tb_norm.hip", "tb_mx.hip", "tb_moe.hip", "tb_kv.hip", "tb_attn.hip")   # libtb.so, one object each
 PROBE_SRC = os.path.join(PKG, "csrc", "probe.hip")
 PROBE_LIB = os.path.join(PKG, "libtb_probe.so")
 INCLUDE = os.path.join(ROOT, "include")
