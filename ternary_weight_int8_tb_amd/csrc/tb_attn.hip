@@ -107,6 +107,14 @@ struct Split<F16, true> {
 };
 __device__ __forceinline__ uint32_t &word(uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// v, of which the compiler does not know that it is v: what is derived from it is derived where it is used, and not kept in
+// registers from before the loops
+__device__ __forceinline__ int opaque(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // ---- units --------------------------------------------------------------------------
 struct Unit {
     int first, n, len;   // the request's first row of q, its new tokens, its length
@@ -264,32 +272,42 @@ __device__ __forceinline__ int fold(int row)
     return D >= 128 ? row & 7 : (row >> 1) & 3;
 }
 
+// The same in all lanes, in scalar registers
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
+{
+    const uint64_t v = (uint64_t)p;
+    return (const uint8_t *)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                             (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
 // 16 keys, one contiguous stretch of a page, to LDS
 template <int D>
 struct Loader {
     static constexpr int kLoads = D / 32;    // of 1 KB
-    static constexpr int kKinds = D >= 256 ? 4 : D >= 128 ? 2 : 1;
-    uint32_t off[kKinds];
+    uint32_t off;                            // of the lane's 16 bytes in a load, at their places in LDS
     __device__ __forceinline__ void init(int lane)
     {
         constexpr int kLanes = D / 8;   // of a row
-#pragma unroll
-        for (int x = 0; x < kKinds; ++x) {
-            const int row = x * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
-            off[x] = (uint32_t)(lane / kLanes * D * 2 + (((c >> 1) ^ fold<D>(row)) << 5) + (c & 1) * 16);
-        }
+        const int row = lane / kLanes, c = lane % kLanes;
+        off = (uint32_t)(row * D * 2 + (((c >> 1) ^ fold<D>(row)) << 5) + (c & 1) * 16);
     }
+    __device__ __forceinline__ void pin() { asm volatile("" : "+v"(off)); }   // as Rows::pin_reads
     // `from` and `to` are the same in all lanes; lane l's 16 bytes go to to + 16 l. The compiler knows of the load's
     // writes to LDS, but not when they are done: for the builtin it waits for all loads at the next read of
     // any of it by ordinary loads, and never for transposing reads. So this is an asm without outputs, and each
     // read of a buffer stands behind a wait of its own (landed()).
     __device__ __forceinline__ void load(const uint8_t *from, lds_t *to) const
     {
+        from = uniform(from);
+        const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)to);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+        for (int i = 0; i < kLoads; ++i) {
+            // rows 64 / kLanes * i on: their fold differs from row 0's in these bits alone
+            const uint32_t turn = (uint32_t)fold<D>(i * (512 / D)) << 5;
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                         ::"s"((uint32_t)(uintptr_t)(to + i * 1024)), "v"(off[i % kKinds]), "s"(from + i * 1024)
+                         ::"s"(lds + i * 1024), "v"(off ^ turn), "s"(from + i * 1024)
                          : "memory");   // m0 is the compiler's to set, and it sets it wherever it needs it
+        }
     }
 };
 // Waits until at most N of the wave's loads are on their way: all but the N last ones have landed.
@@ -302,63 +320,83 @@ __device__ __forceinline__ void landed()
 // The wave's reads of LDS are done.
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int D, class T, bool EXACT>
+// NT column tiles of 16 rows; lane l has, of each, row l % 16.
+template <int D, class T, bool EXACT, int NT>
 struct Rows {
     static constexpr int kQ = D / 32, kO = D / 16, kParts = Split<T, EXACT>::kParts;
     // fp16 weights start at 2^6: small ones keep their bits, and a row whose maximum lags by kLag still fits
-    static constexpr float kBias = sizeof(T) && std::is_same<T, F16>::value ? 6.0f : 0.0f, kLag = 8.0f;
-    uint4 q[kQ][kParts];
-    v4f o[kO];
-    float m, base, l, c;  // running maximum of the scores, the same or 0 before there is one, sum of the lane's weights, the scores' factor
-    int kmin, kmax;       // keys that the lane's row sees
-    uint32_t kread[4], vread[8];
+    static constexpr float kBias = std::is_same<T, F16>::value ? 6.0f : 0.0f, kLag = 8.0f;
+    uint4 q[NT][kQ][kParts];
+    v4f o[NT][kO];
+    float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
+    int pos[NT];                      // the row's position: it sees the keys up to it
+    uint32_t kread, vread;            // the lane's places in a row of K, and of V
+
+    // one factor for all rows, unless they have been scaled
+    static constexpr bool kScaled = EXACT && std::is_same<T, F16>::value;
+    __device__ __forceinline__ float c(const AttnArgs &a, int n) const { return kScaled ? factor[n] : a.scale; }
 
     __device__ __forceinline__ void init_reads(int lane)
     {
-        const int i = lane & 15, g = lane >> 4;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            kread[s] = (uint32_t)(i * D * 2 + ((((2 * s + (g >> 1)) & (D >= 128 ? 7 : 3)) ^ fold<D>(i)) << 5) + (g & 1) * 16);
-        const int row = 4 * g + (i >> 2);
-#pragma unroll
-        for (int d = 0; d < 8; ++d)
-            vread[d] = (uint32_t)(row * D * 2 + (((d & (D >= 128 ? 7 : 3)) ^ fold<D>(row)) << 5) + (i & 3) * 8);
+        const int i = lane & 15, g = lane >> 4, row = 4 * g + (i >> 2);
+        kread = (uint32_t)(i * D * 2 + (((g >> 1) ^ fold<D>(i)) << 5) + (g & 1) * 16);
+        vread = (uint32_t)(row * D * 2 + (fold<D>(row) << 5) + (i & 3) * 8);
     }
+    // Called in the loop over the keys: keeps every place that the reads of a step derive from these two from being
+    // kept in registers of its own
+    __device__ __forceinline__ void pin_reads() { asm volatile("" : "+v"(kread), "+v"(vread)); }
+    // Segments within 256 (or 128) bytes are turned by fold, those beyond stand apart
+    static constexpr int kSegs = D >= 128 ? 8 : 4;
     __device__ __forceinline__ uint4 key(const lds_t *buf, int t, int s) const
     {
-        constexpr int kPer = D >= 128 ? 4 : 2;   // operands of 256 (or 128) bytes of the row
-        return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) v4u *)(buf + kread[s % kPer] + s / kPer * 256 + t * 16 * D * 2));
+        const uint32_t at = (kread ^ (uint32_t)(2 * s % kSegs) << 5) + 2 * s / kSegs * 256;
+        return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) v4u *)(buf + at + t * 16 * D * 2));
     }
     __device__ __forceinline__ uint4 value(const lds_t *buf, int d) const
     {
-        constexpr int kPer = D >= 128 ? 8 : 4;
+        const uint32_t at = (vread ^ (uint32_t)(d % kSegs) << 5) + d / kSegs * 256;
         uint2 w[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            w[t] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                 (__attribute__((address_space(3))) v4s *)(buf + vread[d % kPer] + d / kPer * 256 + t * 16 * D * 2)));
+            w[t] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(buf + at + t * 16 * D * 2)));
         return make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
 
-    // Row `row` of a unit (rows past the last are that one): its q, and what it sees.
-    __device__ __forceinline__ void begin(const AttnArgs &a, const Unit &u, int head, int row, int lane)
+    // Rows row0 .. row0 + 16 NT - 1 of a unit (rows past the last are that one): their q, and what they see.
+    __device__ __forceinline__ void begin(const AttnArgs &a, const Unit &u, int head, int row0, int lane)
     {
-        const int r = min(row, u.n * a.group - 1), tok = r / a.group, h = head * a.group + r - tok * a.group, g = lane >> 4;
-        const int p = u.len - u.n + tok;
-        kmax = max(min(min(u.len, a.width << a.page_shift), p + 1), 0);
-        kmin = a.window ? max(p - a.window + 1, 0) : 0;
-        const size_t at = (size_t)((long long)(u.first + tok) * a.q_row + (long long)h * a.q_head) + 8 * g;
-        c = a.scale;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = min(row0 + 16 * n + (lane & 15), u.n * a.group - 1), tok = r / a.group, h = head * a.group + r - tok * a.group;
+            pos[n] = u.len - u.n + tok;
+            load_q(a, n, (size_t)((long long)(u.first + tok) * a.q_row + (long long)h * a.q_head) + 8 * (lane >> 4));
+        }
+        // loaded here, or the wait for these loads stands in the loop over the keys, where it would also be one for theirs
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int s = 0; s < kQ; ++s)
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                    asm volatile("" : "+v"(q[n][s][x].x), "+v"(q[n][s][x].y), "+v"(q[n][s][x].z), "+v"(q[n][s][x].w));
+            m[n] = -INFINITY;
+            l[n] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kO; ++d)
+                o[n][d] = v4f{};
+        }
+    }
+    __device__ __forceinline__ void load_q(const AttnArgs &a, int n, size_t at)
+    {
         if constexpr (!EXACT) {
 #pragma unroll
             for (int s = 0; s < kQ; ++s)
-                q[s][0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + at + 32 * s);
+                q[n][s][0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + at + 32 * s);
         } else {
             Eight<float> e[kQ];
 #pragma unroll
             for (int s = 0; s < kQ; ++s)
                 e[s].load(static_cast<const float *>(a.q) + at + 32 * s);
-            float f = 1.0f;
             if constexpr (std::is_same<T, F16>::value) {
                 // the row's largest element between 2^9 and 2^10: whatever the row's magnitude, its parts are fp16 numbers
                 float top = 0.0f, v[8];
@@ -374,8 +412,7 @@ struct Rows {
                 const int ex = top > 0.0f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 1), 254) - 127 : 9;
                 // 2^(9 - ex) in two factors, either of which fp32 holds
                 const int half = (9 - ex) / 2;
-                f = __builtin_ldexpf(1.0f, half);
-                const float f2 = __builtin_ldexpf(1.0f, 9 - ex - half);
+                const float f = __builtin_ldexpf(1.0f, half), f2 = __builtin_ldexpf(1.0f, 9 - ex - half);
 #pragma unroll
                 for (int s = 0; s < kQ; ++s) {
                     e[s].get(v);
@@ -384,7 +421,7 @@ struct Rows {
                         v[x] = v[x] * f * f2;
                     e[s].set(v);
                 }
-                c = c / f / f2;
+                factor[n] = a.scale / f / f2;
             }
 #pragma unroll
             for (int s = 0; s < kQ; ++s) {
@@ -396,36 +433,26 @@ struct Rows {
                     Split<T, EXACT>::pair(v[2 * x], v[2 * x + 1], w);
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
-                        word(q[s][p], x) = w[p];
+                        word(q[n][s][p], x) = w[p];
                 }
             }
         }
-        // loaded here, or the wait for these loads stands in the loop over the keys, where it would also be one for theirs
-#pragma unroll
-        for (int s = 0; s < kQ; ++s)
-#pragma unroll
-            for (int x = 0; x < kParts; ++x)
-                asm volatile("" : "+v"(q[s][x].x), "+v"(q[s][x].y), "+v"(q[s][x].z), "+v"(q[s][x].w));
-        m = -INFINITY;
-        base = 0.0f;
-        l = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kO; ++d)
-            o[d] = v4f{};
     }
 
-    // Scores of 32 keys from key0 on: s[t][i] is key 16 t + 4 g + i
-    __device__ __forceinline__ void scores(const lds_t *kb, v4f (&s)[2]) const
+    // Scores of 32 keys: s[n][t][i] is key 16 t + 4 g + i. Operands in batches, one on its way while the other is
+    // multiplied.
+    __device__ __forceinline__ void scores(const lds_t *kb, v4f (&s)[NT][2]) const
     {
-        s[0] = s[1] = v4f{};
-        // operands in batches, one on its way while the other is multiplied
-        constexpr int kBatch = 4, kBatches = 2 * kQ / kBatch;
+        constexpr int kBatch = NT > 1 ? 2 : 4, kBatches = 2 * kQ / kBatch;
         uint4 k[2][kBatch];
         auto read = [&](int b) {
 #pragma unroll
             for (int x = 0; x < kBatch; ++x)
                 k[b & 1][x] = key(kb, x & 1, (b * kBatch + x) >> 1);
         };
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            s[n][0] = s[n][1] = v4f{};
         read(0);
 #pragma unroll
         for (int b = 0; b < kBatches; ++b) {
@@ -436,63 +463,77 @@ struct Rows {
             for (int p = kParts; p-- > 0;)
 #pragma unroll
                 for (int x = 0; x < kBatch; ++x)
-                    s[x & 1] = mfma(k[b & 1][x], q[(b * kBatch + x) >> 1][p], s[x & 1], T());
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        s[n][x & 1] = mfma(k[b & 1][x], q[n][(b * kBatch + x) >> 1][p], s[n][x & 1], T());
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // `gone`: bit t set where the 16 keys t have no page
-    __device__ __forceinline__ bool sees(int key0, int j, int g, uint32_t gone) const
-    {
-        const int k = key0 + (j >> 2) * 16 + 4 * g + (j & 3);
-        return k >= kmin && k < kmax && !(gone >> (j >> 2) & 1);
-    }
-    __device__ __forceinline__ void hide(int key0, int g, uint32_t gone, v4f (&s)[2]) const
+    // Does row n see key k? (Keys from a unit's kend on are seen by none: their values are zeros, and see hide().)
+    __device__ __forceinline__ bool sees(const AttnArgs &a, int n, int k) const { return k <= pos[n] && (!a.window || k > pos[n] - a.window); }
+    // `there`: bit x set where key x of the 32 is one that some row of the unit sees
+    __device__ __forceinline__ void hide(const AttnArgs &a, int key0, int g, uint32_t there, v4f (&s)[NT][2]) const
     {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s[j >> 2][j & 3] = sees(key0, j, g, gone) ? s[j >> 2][j & 3] : -INFINITY;
+        for (int j = 0; j < 8; ++j) {
+            const int x = (j >> 2) * 16 + 4 * g + (j & 3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                s[n][j >> 2][j & 3] = (there >> x & 1) && sees(a, n, key0 + x) ? s[n][j >> 2][j & 3] : -INFINITY;
+        }
     }
     // The weights of 32 keys, and what they do to the maximum and the sum. The maximum follows only when a score
     // exceeds it by kLag: until then weights are larger than one, which costs no bits, and o stays as it is.
     // Scores are subtracted before they are scaled: one fused operation for both would leave the rounding of the
     // maximum's product in the exponent, of any size where scores are large.
-    __device__ __forceinline__ void weigh(const v4f (&s)[2], uint4 (&p)[kParts])
+    __device__ __forceinline__ void weigh(const AttnArgs &a, const v4f (&s)[NT][2], uint4 (&p)[NT][kParts])
     {
-        float top = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
-        top = fmaxf(top, fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        if (__any((top - m) * c > kLag)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float now = fmaxf(m, top);
-            if (now > m) {
-                const float f = __builtin_amdgcn_exp2f((m - now) * c);
-                l *= f;
+        float top[NT];
+        bool more = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            top[n] = fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3]));
+            top[n] = fmaxf(top[n], fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+            more |= (top[n] - m[n]) * c(a, n) > kLag;
+        }
+        if (__any(more)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+                top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+                const float now = fmaxf(m[n], top[n]);
+                const float f = now > m[n] ? __builtin_amdgcn_exp2f((m[n] - now) * c(a, n)) : 1.0f;
+                m[n] = now;
+                l[n] *= f;
 #pragma unroll
                 for (int d = 0; d < kO; ++d)
-                    o[d] *= f;
-                m = base = now;
+                    o[n][d] *= f;
             }
         }
-        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 2][j & 3] - base, c, kBias));
+        for (int n = 0; n < NT; ++n) {
+            const float base = m[n] == -INFINITY ? 0.0f : m[n];   // no key yet: all weights are 0
+            float w[8];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            uint32_t parts[kParts];
-            Split<T, EXACT>::pair(w[2 * x], w[2 * x + 1], parts);
+            for (int j = 0; j < 8; ++j)
+                w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3] - base, c(a, n), kBias));
 #pragma unroll
-            for (int y = 0; y < kParts; ++y)
-                word(p[y], x) = parts[y];
-            if constexpr (EXACT)
-                l += w[2 * x] + w[2 * x + 1];
-            else
-                l = dot2(parts[0], ones(T()), l, T());   // the weights as they are used
+            for (int x = 0; x < 4; ++x) {
+                uint32_t parts[kParts];
+                Split<T, EXACT>::pair(w[2 * x], w[2 * x + 1], parts);
+#pragma unroll
+                for (int y = 0; y < kParts; ++y)
+                    word(p[n][y], x) = parts[y];
+                if constexpr (EXACT)
+                    l[n] += w[2 * x] + w[2 * x + 1];
+                else
+                    l[n] = dot2(parts[0], ones(T()), l[n], T());   // the weights as they are used
+            }
         }
     }
-    __device__ __forceinline__ void add(const lds_t *vb, const uint4 (&p)[kParts])
+    __device__ __forceinline__ void add(const lds_t *vb, const uint4 (&p)[NT][kParts])
     {
-        constexpr int kBatch = 4, kBatches = kO / kBatch;
+        constexpr int kBatch = NT > 1 ? 2 : 4, kBatches = kO / kBatch;
         uint4 v[2][kBatch];
         auto read = [&](int b) {
 #pragma unroll
@@ -509,100 +550,86 @@ struct Rows {
             for (int y = kParts; y-- > 0;)
 #pragma unroll
                 for (int x = 0; x < kBatch; ++x)
-                    o[b * kBatch + x] = mfma(v[b & 1][x], p[y], o[b * kBatch + x], T());
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        o[n][b * kBatch + x] = mfma(v[b & 1][x], p[n][y], o[n][b * kBatch + x], T());
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // The same where some keys are hidden from some rows. A weight of zero does not hide a value that is not
-    // finite: keys from `lo` to `hi` are the ones that any row of the unit sees, others are taken for zeros; and
-    // if `mixed`, some of these hidden from some rows, keys with such values are added one at a time, to the
-    // rows that see them.
-    __device__ __forceinline__ void add_some(const lds_t *vb, const uint4 (&p)[kParts], int key0, int g, uint32_t gone, int lo, int hi, bool mixed)
+    // The elements of key k's values (in memory at v) that are not finite, into the rows that see it: LDS holds zeros in their
+    // place, as a weight of 0 would not keep them from the other rows.
+    __device__ __forceinline__ void poison(const AttnArgs &a, int k, const uint8_t *v, int lane)
     {
-        auto mask_of = [&](uint32_t keys) {   // bit 16 t + k: key k of tile t
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint32_t two = keys >> ((x >> 1) * 16 + 4 * g + (x & 1) * 2);
-                w[x] = (two & 1 ? 0xffffu : 0u) | (two & 2 ? 0xffff0000u : 0u);
-            }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        };
-        auto masked = [&](uint4 v, uint4 k) { return make_uint4(v.x & k.x, v.y & k.y, v.z & k.z, v.w & k.w); };
-        // keys lo .. hi - 1 as bits
-        auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-        uint32_t keep = low_bits(hi - key0) & ~low_bits(lo - key0);
-        keep &= ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
-        uint32_t strange = 0;   // bit j: the lane's key j has a value that is not finite
-        if (mixed) {
-            const uint4 k = mask_of(keep);
-#pragma unroll 2
-            for (int d = 0; d < kO; ++d) {
-                const uint4 v = masked(value_at(vb, d), k);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    constexpr uint32_t e = exponents(T());
-                    strange |= ((w[x] & e & 0xffffu) == (e & 0xffffu) ? 1u << (2 * x) : 0u) |
-                               ((w[x] & e & 0xffff0000u) == (e & 0xffff0000u) ? 2u << (2 * x) : 0u);
-                }
-            }
-        }
-        uint32_t apart = 0;
-        if (__any(strange)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const unsigned long long set = __ballot(strange >> j & 1);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    apart |= (set >> (16 * x) & 0xffffu) ? 1u << ((j >> 2) * 16 + 4 * x + (j & 3)) : 0u;
-            }
-        }
-        const uint4 k = mask_of(keep & ~apart);
+        v += 8 * (lane >> 4);
 #pragma unroll
         for (int d = 0; d < kO; ++d) {
-            const uint4 v = masked(value(vb, d), k);
+            asm volatile("" : "+v"(v)::"memory");   // one load at a time: the loop over the keys has no registers to spare
+            const uint2 two = *reinterpret_cast<const uint2 *>(v + 32 * d);
+            float e[4];
+            unpack(two.x, e[0], e[1], T());
+            unpack(two.y, e[2], e[3], T());
 #pragma unroll
-            for (int y = kParts; y-- > 0;)
-                o[d] = mfma(v, p[y], o[d], T());
-        }
-        while (apart) {
-            const int one = __builtin_ctz(apart);
-            apart &= apart - 1;
-            const uint4 ko = mask_of(1u << one);
-            const int kk = key0 + one;
-            const bool seen = kk >= kmin && kk < kmax;
-#pragma unroll
-            for (int d = 0; d < kO; ++d) {
-                const uint4 v = masked(value(vb, d), ko);
-                v4f x = o[d];
-#pragma unroll
-                for (int y = kParts; y-- > 0;)
-                    x = mfma(v, p[y], x, T());
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    o[d][i] = seen ? x[i] : o[d][i];
-            }
+                    o[n][d][i] += sees(a, n, k) && !(fabsf(e[i]) < INFINITY) ? e[i] : 0.0f;
         }
     }
-    // value() of a d that is not known at compile time
-    __device__ __forceinline__ uint4 value_at(const lds_t *buf, int d) const
-    {
-        constexpr int kPer = D >= 128 ? 8 : 4;
-        const uint32_t at = (vread[0] ^ ((uint32_t)(d % kPer) << 5)) + d / kPer * 256;
-        uint2 w[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            w[t] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(buf + at + t * 16 * D * 2)));
-        return make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
-    }
-    // the row's sum, in all four lanes that share it
+    // the rows' sums, in all four lanes that share one
     __device__ __forceinline__ void end()
     {
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+        }
     }
 };
+
+// Zeros in LDS for the values of keys that no row of the unit sees (memory that no one has written, or another
+// request's), and for those that are not finite: a weight of 0 would not keep either from a row that does not see the key.
+// KEYS keys of D elements from `buf` on, bit x of `there` set if key x is seen; taken by LANES threads of which
+// this is number `me`. Returns the keys that are seen and have such values (see Rows::poison), as far as this thread has met them.
+template <int D, class T, int LANES, int KEYS>
+__device__ __forceinline__ uint64_t clean(lds_t *buf, uint64_t there, int me)
+{
+    constexpr int kLanes = D / 8, kPasses = KEYS * kLanes / LANES;   // threads of a row
+    static_assert(LANES % kLanes == 0 && kPasses >= 1, "whole rows");
+    uint64_t strange = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int x = pass * (LANES / kLanes) + me / kLanes;
+        __attribute__((address_space(3))) v4u *at = (__attribute__((address_space(3))) v4u *)(buf + x * D * 2 + me % kLanes * 16);
+        v4u v = *at;
+        const bool seen = there >> x & 1;
+        bool odd = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            constexpr uint32_t e = exponents(T()), lo = e & 0xffffu, hi = e & 0xffff0000u;
+            const uint32_t bad = ((v[w] & lo) == lo ? 0xffffu : 0u) | ((v[w] & hi) == hi ? 0xffff0000u : 0u);
+            odd |= bad != 0;
+            v[w] = seen ? v[w] & ~bad : 0u;
+        }
+        if (odd || !seen)
+            *at = v;
+        if (odd && seen)
+            strange |= 1ull << x;
+    }
+    return strange;
+}
+// keys lo .. hi - 1 as bits of those from key0 on
+__device__ __forceinline__ uint64_t key_bits(int lo, int hi, int key0)
+{
+    auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+    return below(hi - key0) & ~below(lo - key0);
+}
+__device__ __forceinline__ uint64_t any_of(uint64_t bits)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        bits |= (uint64_t)__shfl_xor((unsigned long long)bits, d);
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(bits >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)bits);
+}
 
 // ---- results ------------------------------------------------------------------------
 // o[0..3] / l, gated, as elements d .. d + 3 of the unit's row `row`
@@ -667,7 +694,7 @@ template <int D, class T, class Q>
 __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narrow_kernel(AttnArgs a)
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
-    using R = Rows<D, T, kExact>;
+    using R = Rows<D, T, kExact, 1>;
     constexpr int kBuf = kBlk * D * 2;
     // arrays of their own: a read of one then waits for no load of the other
     __shared__ __align__(128) uint8_t kbuf[kNarrowWaves * kBuf];
@@ -727,7 +754,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 }
                 return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
             };
-            size_t at[2];
+            size_t at[2] = {0, 0};
             uint32_t gone = 0;
             if (blk * kBlk < hi) {
 #pragma unroll
@@ -740,7 +767,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 for (int t = 0; t < 2; ++t)
                     loader.load(a.v + at[t], vb + t * 16 * D * 2);
             }
-            rows.begin(a, u, head, row0 + i, lane);   // behind the loads of keys and values: waited for once, with them
+            rows.begin(a, u, head, row0, lane);   // behind the loads of keys and values: waited for once, with them
             while (blk * kBlk < hi) {
                 const int key0 = blk * kBlk, next = blk + kNarrowWaves;
                 const bool more = next * kBlk < hi;
@@ -751,7 +778,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                     for (int t = 0; t < 2; ++t)
                         nat[t] = place(next * kBlk + 16 * t, t, ngone);
                 }
-                v4f s[2];
+                v4f s[1][2];
                 landed<2 * Loader<D>::kLoads>();   // all but the values, which were asked for last
                 rows.scores(kb, s);
                 lds_read();
@@ -760,20 +787,26 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                     for (int t = 0; t < 2; ++t)
                         loader.load(a.k + nat[t], kb + t * 16 * D * 2);
                 }
+                const bool whole = key0 >= some_lo && key0 + kBlk <= some_hi && !gone;
+                const uint32_t there = (uint32_t)key_bits(u.kbeg, u.kend, key0) & ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
+                if (!whole)
+                    rows.hide(a, key0, g, there, s);
+                uint4 p[1][R::kParts];
+                rows.weigh(a, s, p);
                 if (more)   // the next keys may be on their way
                     landed<2 * Loader<D>::kLoads>();
                 else
                     landed<0>();
-                const bool whole = key0 >= some_lo && key0 + kBlk <= some_hi && !gone;
-                if (!whole)
-                    rows.hide(key0, g, gone, s);
-                uint4 p[R::kParts];
-                rows.weigh(s, p);
-                if (whole)
-                    rows.add(vb, p);
-                else
-                    rows.add_some(vb, p, key0, g, gone, u.kbeg, u.kend,
-                                  min(key0 + kBlk, u.kend) > some_hi || max(key0, u.kbeg) < some_lo);
+                uint64_t strange = 0;
+                if (!whole) {
+                    strange = any_of(clean<D, T, 64, kBlk>(vb, there, lane));
+                    lds_read();
+                }
+                for (; strange; strange &= strange - 1) {
+                    const int x = __builtin_ctzll(strange), t = x >> 4;
+                    rows.poison(a, key0 + x, a.v + (t ? at[1] : at[0]) + (x & 15) * (D * 2), lane);
+                }
+                rows.add(vb, p);
                 lds_read();
                 if (more) {
 #pragma unroll
@@ -781,26 +814,27 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                         loader.load(a.v + nat[t], vb + t * 16 * D * 2);
                 }
                 gone = ngone;
+                at[0] = nat[0], at[1] = nat[1];
                 blk = next;
             }
             rows.end();
 
             // the waves' sums become one, in the order of the waves
             if (g == 0) {
-                m_s[wave][i] = rows.m;
-                l_s[wave][i] = rows.l;
-                c_s[i] = rows.c;   // the same in all waves
+                m_s[wave][i] = rows.m[0];
+                l_s[wave][i] = rows.l[0];
+                c_s[i] = rows.c(a, 0);   // the same in all waves
             }
             __syncthreads();
             float top = m_s[0][i];
 #pragma unroll
             for (int w = 1; w < kNarrowWaves; ++w)
                 top = fmaxf(top, m_s[w][i]);
-            const float f = rows.m == top ? 1.0f : __builtin_amdgcn_exp2f((rows.m - top) * rows.c);
+            const float f = rows.m[0] == top ? 1.0f : __builtin_amdgcn_exp2f((rows.m[0] - top) * rows.c(a, 0));
             float *mine = reinterpret_cast<float *>(kbuf) + wave * kNarrowRows * D;
 #pragma unroll
             for (int d = 0; d < R::kO; ++d)
-                *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[d] * f;
+                *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[0][d] * f;
             __syncthreads();
             const bool begins = into == 0, ends = into + take == u.steps;
             for (int x = tid; x < kNarrowRows * D / 4; x += kNarrowWaves * 64) {
@@ -860,6 +894,214 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
         meta->parts = 0;
 }
 
+// ---- many rows: a unit has a tile of rows for each wave, which all read the same keys ----------------
+// 64 keys and their values at a time, in one of two buffers while the other is filled. With NT column tiles each
+// operand that is read from LDS enters NT instructions: at two, reading takes as long as multiplying (128
+// bytes a cycle for four SIMDs' 32 cycles per KB).
+constexpr int kWideStep = 64;
+constexpr int kWideWaves = 8;
+constexpr int wide_tiles(bool exact) { return exact ? 1 : 2; }
+constexpr int wide_rows(bool exact) { return kWideWaves * wide_tiles(exact) * 16; }
+constexpr int wide_per_cu(int dim, bool exact) { return dim == 64 && !exact ? 2 : 1; }
+
+template <int D, class T, class Q>
+__global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q, float>::value)) void attn_wide_kernel(AttnArgs a)
+{
+    constexpr bool kExact = std::is_same<Q, float>::value;
+    constexpr int kWaves = kWideWaves, kTiles = wide_tiles(kExact), kRows = wide_rows(kExact);
+    using R = Rows<D, T, kExact, kTiles>;
+    constexpr int kGroup = 16 * D * 2, kBuf = kWideStep * D * 2, kGroups = kWideStep / 16;
+    __shared__ __align__(128) uint8_t kbuf[2 * kBuf];
+    __shared__ __align__(128) uint8_t vbuf[2 * kBuf];
+    __shared__ int chunk_s[kWaves * 64];
+    __shared__ int wave_s[kWaves], found_s[3];
+    __shared__ unsigned long long strange_s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
+    const int slots = gridDim.x, slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
+    if (tid == 0)
+        strange_s = 0;
+    Start st;
+    unsigned per;
+    find_start<kRows, kWideStep, kWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
+    unsigned line = (unsigned)slot * per;
+    const unsigned end = min(line + per, (unsigned)st.all * (unsigned)a.kv_heads);
+    Meta *meta = reinterpret_cast<Meta *>(a.meta) + slot;
+    int parts = 0;
+    if (line < end) {
+        const const_ints table = (const_ints)a.table;
+        int head = (int)(line / (unsigned)st.all), req = st.req, into = st.into;
+        Unit u;
+        u.tile = st.tile;
+        Loader<D> loader;
+        loader.init(lane);
+        R rows;
+        rows.init_reads(lane);
+        for (;;) {
+            request_of(a, req, u.first, u.n, u.len);
+            u.first = __builtin_amdgcn_readfirstlane(u.first);
+            u.n = __builtin_amdgcn_readfirstlane(u.n);
+            u.len = __builtin_amdgcn_readfirstlane(u.len);
+            span<kRows, kWideStep>(a, u);
+            const int take = (int)min((unsigned)(u.steps - into), end - line);
+            const int unit0 = u.tile * kRows, nrows = min(u.n * a.group - unit0, kRows);
+            const int row0 = unit0 + wave * kTiles * 16;
+            const bool active = row0 < unit0 + nrows;   // the wave has rows
+            // The wave's rows all see the keys from some_lo on up to some_hi; any of them, those from any_lo on up to any_hi.
+            int some_lo = 0, some_hi = 0, any_lo = 0, any_hi = 0;
+            if (active) {
+                const int last = min(row0 + kTiles * 16, unit0 + nrows) - 1;
+                const int p0 = u.len - u.n + row0 / a.group, p1 = u.len - u.n + last / a.group;
+                some_hi = max(min(u.kend, p0 + 1), 0);
+                any_hi = max(min(u.kend, p1 + 1), 0);
+                if (a.window) {
+                    some_lo = max(p1 - a.window + 1, 0);
+                    any_lo = max(p0 - a.window + 1, 0);
+                }
+            }
+            const int first = u.s0 + into;
+            // all rows of the unit see the keys from unit_lo on up to unit_hi
+            const int unit_hi = min(u.kend, u.len - u.n + unit0 / a.group + 1);
+            const int unit_lo = a.window ? u.len - u.n + (unit0 + nrows - 1) / a.group - a.window + 1 : 0;
+            // The pages of a step's groups of 16 keys
+            auto ids_of = [&](int step, int (&id)[kGroups]) {
+#pragma unroll
+                for (int x = 0; x < kGroups; ++x) {
+                    const int key = step * kWideStep + 16 * x;
+                    id[x] = key < u.kend ? table[(size_t)req * a.width + (key >> a.page_shift)] : -1;
+                }
+            };
+            auto at_of = [&](int id, int key) {
+                id = (unsigned)id < (unsigned)a.pages ? id : 0;
+                return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
+            };
+            // wave 2 x loads the keys of group x, wave 2 x + 1 its values
+            static_assert(2 * kGroups == kWaves, "a group's keys or values per wave");
+            auto load = [&](int step, int b, const int (&id)[kGroups]) {
+                const int x = wave >> 1;
+                const size_t at = at_of(x == 0 ? id[0] : x == 1 ? id[1] : x == 2 ? id[2] : id[3], step * kWideStep + 16 * x);
+                loader.load((wave & 1 ? a.v : a.k) + at, (wave & 1 ? (lds_t *)vbuf : (lds_t *)kbuf) + b * kBuf + x * kGroup);
+            };
+            int id[kGroups], next_id[kGroups];
+            ids_of(first, id);
+            load(first, 0, id);
+            if (take > 1)
+                ids_of(first + 1, next_id);
+            rows.begin(a, u, head, row0, opaque(lane));
+            landed<0>();
+            __syncthreads();
+            for (int x = 0; x < take; ++x) {
+                const int b = x & 1, step = first + x, step0 = step * kWideStep;
+                uint64_t there = key_bits(u.kbeg, u.kend, step0), strange = 0;
+#pragma unroll
+                for (int z = 0; z < kGroups; ++z)
+                    there &= (unsigned)id[z] < (unsigned)a.pages ? ~0ull : ~(0xffffull << (16 * z));
+                if (step0 < unit_lo || step0 + kWideStep > unit_hi || ~there) {
+                    const uint64_t odd = any_of(clean<D, T, kWaves * 64, kWideStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
+                    if (odd && lane == 0)
+                        atomicOr(&strange_s, (unsigned long long)odd);
+                    __syncthreads();
+                    strange = any_of(strange_s);
+                }
+                if (x + 1 < take) {
+                    loader.pin();
+                    load(step + 1, b ^ 1, next_id);
+                }
+#pragma unroll 1
+                for (int y = 0; y < kWideStep / kBlk; ++y) {
+                    const int key0 = step0 + y * kBlk;
+                    if (key0 >= any_hi || key0 + kBlk <= any_lo)
+                        continue;
+                    const lds_t *kb = (const lds_t *)kbuf + b * kBuf + y * 2 * kGroup, *vb = (const lds_t *)vbuf + b * kBuf + y * 2 * kGroup;
+                    const uint32_t mine = (uint32_t)(there >> (32 * y));
+                    v4f s[kTiles][2];
+                    rows.pin_reads();
+                    rows.scores(kb, s);
+                    if (key0 < some_lo || key0 + kBlk > some_hi || ~mine)
+                        rows.hide(a, key0, g, mine, s);
+                    uint4 p[kTiles][R::kParts];
+                    rows.weigh(a, s, p);
+                    for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
+                        const int z = __builtin_ctz(odd), group = 2 * y + (z >> 4);
+                        rows.poison(a, key0 + z, a.v + at_of(group == 0 ? id[0] : group == 1 ? id[1] : group == 2 ? id[2] : id[3], key0 + z), lane);
+                    }
+                    rows.add(vb, p);
+                }
+#pragma unroll
+                for (int z = 0; z < kGroups; ++z)
+                    id[z] = next_id[z];
+                if (x + 2 < take)
+                    ids_of(step + 2, next_id);
+                landed<0>();
+                __syncthreads();
+                if (strange) {
+                    if (tid == 0)
+                        strange_s = 0;
+                    __syncthreads();
+                }
+            }
+            rows.end();
+            const bool begins = into == 0, ends = into + take == u.steps;
+            // Through LDS, a column tile at a time, so that whole rows are written. (Both buffers have been read; a wave
+            // reads what its own lanes wrote.)
+            float *mine = reinterpret_cast<float *>(wave < kWaves / 2 ? kbuf : vbuf) + wave % (kWaves / 2) * (16 * D);
+            const int own = opaque(lane), i = own & 15, g = own >> 4;
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                const int r0 = wave * kTiles * 16 + 16 * n;   // of the unit
+#pragma unroll
+                for (int d = 0; d < R::kO; ++d)
+                    *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[n][d];
+                lds_read();
+                const float ln = rows.l[n], mn = rows.m[n], cn = rows.c(a, n);
+#pragma unroll 1
+                for (int x = own; x < 4 * D; x += 64) {
+                    const int r = x / (D / 4), ch = x % (D / 4);
+                    const v4f o = *reinterpret_cast<const v4f *>(mine + r * D + (ch ^ r) * 4);
+                    const float l = __shfl(ln, r), m = __shfl(mn, r), c = __shfl(cn, r);
+                    if (r0 + r >= nrows)
+                        continue;
+                    if (begins && ends) {
+                        put_out<Q, D>(a, u.first, unit0 + r0 + r, head, ch * 4, o, l);
+                    } else {
+                        float *part = part_of<kRows, D>(a, slot, begins);
+                        *reinterpret_cast<v4f *>(part + (r0 + r) * D + ch * 4) = o;
+                        if (ch == 0) {
+                            part[kRows * D + r0 + r] = m;
+                            part[kRows * D + kRows + r0 + r] = l;
+                            part[kRows * D + 2 * kRows + r0 + r] = c;
+                        }
+                    }
+                }
+                lds_read();
+            }
+            __syncthreads();
+            if (begins && !ends) {
+                parts = (int)((line + (unsigned)u.steps - 1u) / per) - slot + 1;
+                if (tid == 0)
+                    *meta = Meta{parts, head, u.first, u.n * a.group, unit0, {}};
+            }
+            line += take;
+            if (line >= end)
+                break;
+            into = 0;
+            ++u.tile;
+            if (u.tile * kRows >= u.n * a.group) {
+                u.tile = 0;
+                int f, n, len;
+                do {
+                    if (++req == a.requests) {
+                        req = 0;
+                        ++head;
+                    }
+                    request_of(a, req, f, n, len);
+                } while (__builtin_amdgcn_readfirstlane(n) == 0);   // line < end: there is one
+            }
+        }
+    }
+    if (parts == 0 && tid == 0)
+        meta->parts = 0;
+}
+
 // ---- units that a border cut ---------------------------------------------------------
 // Workgroup (slot, y) joins 1024 / D rows of the unit that begins in the slot, if it ends in another:
 // o = sum_j 2^(c (m_j - m)) o_j and l likewise, over the parts in order.
@@ -890,21 +1132,37 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
 }
 
 // ---- host ---------------------------------------------------------------------------
+// Which kernel: rows of 16 while the requests have few rows of a kv head each, on average.
+bool is_wide(int group, int requests, int tokens) { return (long long)tokens * group > 16ll * requests; }
+
 // As many workgroups as the chip's 256 CUs hold at a time: a constant, as the order of the sums must not depend
 // on a partition's size.
-int slots_of(int dim) { return 256 * narrow_per_cu(dim); }
+int slots_of(bool wide, int dim, bool exact) { return 256 * (wide ? wide_per_cu(dim, exact) : narrow_per_cu(dim)); }
 constexpr size_t kMetaBytes = 768 * sizeof(Meta);
 
-size_t workspace(int dim) { return kMetaBytes + (size_t)slots_of(dim) * 2 * kNarrowRows * (dim + 3) * 4; }
+size_t workspace(bool wide, int dim, bool exact)
+{
+    const int rows = wide ? wide_rows(exact) : kNarrowRows;
+    return kMetaBytes + (size_t)slots_of(wide, dim, exact) * 2 * rows * (dim + 3) * 4;
+}
 
 template <int D, class T, class Q>
 int launch(const AttnArgs &a, hipStream_t st)
 {
-    const int slots = slots_of(D);
-    hipLaunchKernelGGL((attn_narrow_kernel<D, T, Q>), dim3(slots), dim3(kNarrowWaves * 64), 0, st, a);
+    constexpr bool kExact = std::is_same<Q, float>::value;
+    const bool wide = is_wide(a.group, a.requests, a.tokens);
+    const int slots = slots_of(wide, D, kExact);
+    if (wide)
+        hipLaunchKernelGGL((attn_wide_kernel<D, T, Q>), dim3(slots), dim3(kWideWaves * 64), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_narrow_kernel<D, T, Q>), dim3(slots), dim3(kNarrowWaves * 64), 0, st, a);
     if (hipGetLastError() != hipSuccess)
         return TB_EHIP;
-    hipLaunchKernelGGL((attn_join_kernel<kNarrowRows, D, Q>), dim3(slots, kNarrowRows * D / 1024), dim3(256), 0, st, a);
+    constexpr int kRows = wide_rows(kExact);
+    if (wide)
+        hipLaunchKernelGGL((attn_join_kernel<kRows, D, Q>), dim3(slots, kRows * D / 1024), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<kNarrowRows, D, Q>), dim3(slots, kNarrowRows * D / 1024), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
@@ -929,7 +1187,7 @@ extern "C" size_t tb_attn_paged_workspace_bytes(const tb_kv_cache *cache, int he
 {
     if (!cache || !shapes_ok(*cache, heads, dtype, requests, tokens) || !runs(*cache, heads, requests, tokens))
         return 0;
-    return workspace(cache->dim);
+    return workspace(is_wide(heads / cache->kv_heads, requests, tokens), cache->dim, dtype == TB_F32);
 }
 
 extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,
@@ -945,7 +1203,7 @@ extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_k
     if (!qb || (gate && !gb))
         return TB_EINVAL;
     const bool can = runs(*cache, q->heads, requests, tokens);
-    const size_t need = can ? workspace(dim) : 0;
+    const size_t need = can ? workspace(is_wide(q->heads / cache->kv_heads, requests, tokens), dim, q->dtype == TB_F32) : 0;
     tbh::Arg a[9] = {{q->data, qb, false},
                      {cache->k, tbh::cache_bytes(*cache), false},
                      {cache->v, tbh::cache_bytes(*cache), false},
