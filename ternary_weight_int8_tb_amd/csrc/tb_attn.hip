@@ -43,6 +43,7 @@ struct AttnArgs {
     const uint8_t *k, *v;
     const int32_t *table, *offsets, *lengths;
     int pages, page_shift, width, kv_heads, group, requests, tokens, window;
+    uint32_t group_mul, group_shift;   // x / group = (x + mulhi(x, mul)) >> shift, for x < 2^31
     float scale;   // times log2(e)
     void *out;
     int32_t *meta;
@@ -115,12 +116,18 @@ __device__ __forceinline__ int opaque(int v)
     return v;
 }
 
+__device__ __forceinline__ int by_group(const AttnArgs &a, int x)
+{
+    return (int)((__umulhi((uint32_t)x, a.group_mul) + (uint32_t)x) >> a.group_shift);
+}
+
 // ---- units --------------------------------------------------------------------------
 struct Unit {
     int first, n, len;   // the request's first row of q, its new tokens, its length
     int tile;
     int kbeg, kend;      // keys that any of its rows sees
     int s0, steps;       // its first step, in steps from key 0 on, and their number (one at least)
+    int cost;            // what it takes on the line of units: its steps, and what beginning and ending it takes, in steps
 };
 
 __device__ __forceinline__ void request_of(const AttnArgs &a, int r, int &first, int &n, int &len)
@@ -134,15 +141,16 @@ __device__ __forceinline__ int tiles_of(const AttnArgs &a, int n)
 {
     return (n * a.group + ROWS - 1) / ROWS;
 }
-template <int ROWS, int STEP>
+template <int ROWS, int STEP, int EXTRA>
 __device__ __forceinline__ void span(const AttnArgs &a, Unit &u)
 {
     const int r0 = u.tile * ROWS, r1 = min(r0 + ROWS, u.n * a.group) - 1;
-    const int p0 = u.len - u.n + r0 / a.group, p1 = u.len - u.n + r1 / a.group;
+    const int p0 = u.len - u.n + by_group(a, r0), p1 = u.len - u.n + by_group(a, r1);
     u.kend = max(min(min(u.len, a.width << a.page_shift), p1 + 1), 0);
     u.kbeg = a.window ? min(max(p0 - a.window + 1, 0), u.kend) : 0;
     u.s0 = u.kbeg / STEP;
     u.steps = max((u.kend + STEP - 1) / STEP - u.s0, 1);
+    u.cost = u.steps + EXTRA;
 }
 
 // Sum over the threads before this one, and over all.
@@ -171,15 +179,82 @@ __device__ __forceinline__ int scan(int v, int *wave_s, int &total)
 }
 
 struct Start {
-    int all;             // steps of all units of a kv head
-    int req, tile, into; // the unit of the slot's first step, and its steps before that
+    int all;             // cost of all units of a kv head
+    int req, tile, into; // the unit where the slot's stretch of the line begins, and the line's place in it
+};
+
+// A thread's walk along the tiles of the requests.
+template <int ROWS, int STEP, int EXTRA>
+struct Walk {
+    int r, left;   // the request, and its tiles from the current one on
+    Unit u;
+    __device__ __forceinline__ void open(const AttnArgs &a)
+    {
+        request_of(a, r, u.first, u.n, u.len);
+        left = tiles_of<ROWS>(a, u.n);
+        u.tile = 0;
+    }
+    __device__ __forceinline__ void next(const AttnArgs &a)
+    {
+        ++u.tile;
+        if (--left == 0) {
+            while (++r < a.requests) {
+                open(a);
+                if (left)
+                    break;
+            }
+        }
+    }
 };
 
 // Every workgroup lays the whole line of units out for itself: a few thousand of them at most, a handful per
 // thread, which is less than a launch for a plan would take.
-template <int ROWS, int STEP, int WAVES>
+template <int ROWS, int STEP, int EXTRA, int WAVES>
 __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slot, int *chunk_s, int *wave_s, int *found_s, Start &st, unsigned &per)
 {
+    using W = Walk<ROWS, STEP, EXTRA>;
+    // the host has checked that the whole line is shorter than 2^31
+    auto share_of = [&](int all) { return max(((unsigned)all * (unsigned)a.kv_heads + (unsigned)slots - 1u) / (unsigned)slots, 1u); };
+    if (a.requests <= 64 && a.tokens <= a.requests) {
+        // a token for each request at most, as in decoding: a wave looks at them alone
+        const int lane = threadIdx.x & 63;
+        W w;
+        w.r = lane;
+        int cost = 0;
+        if (lane < a.requests) {
+            w.open(a);
+            while (w.r == lane && w.left) {
+                span<ROWS, STEP, EXTRA>(a, w.u);
+                cost += w.u.cost;
+                ++w.u.tile, --w.left;
+            }
+        }
+        int sum = cost;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(sum, d);
+            sum += lane >= d ? up : 0;
+        }
+        st.all = __builtin_amdgcn_readlane(sum, 63);
+        per = share_of(st.all);
+        if (st.all == 0)
+            return;
+        const int want = (int)((unsigned)slot * per % (unsigned)st.all);
+        const int at = __builtin_ctzll(__ballot(sum > want));   // the request: want < st.all
+        st.req = at;
+        st.into = want - __builtin_amdgcn_readlane(sum - cost, at);
+        w.r = at;
+        w.open(a);
+        for (;; ++w.u.tile) {
+            span<ROWS, STEP, EXTRA>(a, w.u);
+            if (st.into < w.u.cost || --w.left == 0)
+                break;
+            st.into -= w.u.cost;
+        }
+        st.tile = __builtin_amdgcn_readfirstlane(w.u.tile);
+        st.into = __builtin_amdgcn_readfirstlane(st.into);
+        return;
+    }
     constexpr int kThreads = WAVES * 64;
     const int tid = threadIdx.x, chunk = (a.requests + kThreads - 1) / kThreads;
     const int q0 = min(tid * chunk, a.requests), q1 = min(q0 + chunk, a.requests);
@@ -193,8 +268,7 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
     __syncthreads();
     const int share = (total + kThreads - 1) / kThreads, t0 = min(tid * share, total), t1 = min(t0 + share, total);
     // the chunk, then the request, of tile t0
-    int r = 0, left = 0;   // left: tiles of r from the current one on
-    Unit u{};
+    W w;
     auto locate = [&]() {
         int lo = 0, hi = kThreads;
         while (hi - lo > 1) {
@@ -204,57 +278,42 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
             else
                 hi = mid;
         }
-        r = lo * chunk;
         int t = t0 - chunk_s[lo];
-        for (;; ++r) {   // t0 < total: the chunk holds it
-            request_of(a, r, u.first, u.n, u.len);
-            left = tiles_of<ROWS>(a, u.n);
-            if (t < left || r + 1 >= a.requests)
+        for (w.r = lo * chunk;; ++w.r) {   // t0 < total: the chunk holds it
+            w.open(a);
+            if (t < w.left || w.r + 1 >= a.requests)
                 break;
-            t -= left;
+            t -= w.left;
         }
-        u.tile = t;
-        left -= t;
+        w.u.tile = t;
+        w.left -= t;
     };
-    auto next = [&]() {
-        ++u.tile;
-        if (--left == 0) {
-            while (++r < a.requests) {
-                request_of(a, r, u.first, u.n, u.len);
-                left = tiles_of<ROWS>(a, u.n);
-                if (left)
-                    break;
-            }
-            u.tile = 0;
-        }
-    };
-    int steps = 0;
+    int cost = 0;
     if (t0 < t1) {
         locate();
         for (int t = t0; t < t1; ++t) {
-            span<ROWS, STEP>(a, u);
-            steps += u.steps;
+            span<ROWS, STEP, EXTRA>(a, w.u);
+            cost += w.u.cost;
             if (t + 1 < t1)
-                next();
+                w.next(a);
         }
     }
-    int at = scan<WAVES>(steps, wave_s, st.all);
-    // the host has checked that the whole line has less than 2^31 steps
-    per = max(((unsigned)st.all * (unsigned)a.kv_heads + (unsigned)slots - 1u) / (unsigned)slots, 1u);
+    int at = scan<WAVES>(cost, wave_s, st.all);
+    per = share_of(st.all);
     if (st.all == 0)
         return;
     const int want = (int)((unsigned)slot * per % (unsigned)st.all);
-    if (t0 < t1 && at <= want && want < at + steps) {
+    if (t0 < t1 && at <= want && want < at + cost) {
         locate();
         for (int t = t0; t < t1; ++t) {
-            span<ROWS, STEP>(a, u);
-            if (want < at + u.steps)
+            span<ROWS, STEP, EXTRA>(a, w.u);
+            if (want < at + w.u.cost)
                 break;
-            at += u.steps;
-            next();
+            at += w.u.cost;
+            w.next(a);
         }
-        found_s[0] = r;
-        found_s[1] = u.tile;
+        found_s[0] = w.r;
+        found_s[1] = w.u.tile;
         found_s[2] = want - at;
     }
     __syncthreads();
@@ -367,7 +426,7 @@ struct Rows {
     {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = min(row0 + 16 * n + (lane & 15), u.n * a.group - 1), tok = r / a.group, h = head * a.group + r - tok * a.group;
+            const int r = min(row0 + 16 * n + (lane & 15), u.n * a.group - 1), tok = by_group(a, r), h = head * a.group + r - tok * a.group;
             pos[n] = u.len - u.n + tok;
             load_q(a, n, (size_t)((long long)(u.first + tok) * a.q_row + (long long)h * a.q_head) + 8 * (lane >> 4));
         }
@@ -636,7 +695,7 @@ __device__ __forceinline__ uint64_t any_of(uint64_t bits)
 template <class Q, int D>
 __device__ __forceinline__ void put_out(const AttnArgs &a, int first, int group_row, int head, int d, v4f o, float l)
 {
-    const int tok = group_row / a.group, h = head * a.group + group_row - tok * a.group;
+    const int tok = by_group(a, group_row), h = head * a.group + group_row - tok * a.group;
     const size_t t = (size_t)(first + tok);
     float v[4];
 #pragma unroll
@@ -686,6 +745,7 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int slot, bool begi
 // A wave takes every fourth block of 32 keys, through buffers of its own: no barriers, and a wave's next keys are
 // on their way while it multiplies its values, and the other way round.
 constexpr int kNarrowWaves = 4, kNarrowRows = 16, kNarrowStep = kNarrowWaves * kBlk;
+constexpr int kNarrowExtra = 2;
 
 // workgroups of a CU: what LDS holds (128, 64 or 32 KB each), and registers
 constexpr int narrow_per_cu(int dim) { return dim == 256 ? 1 : dim == 128 ? 2 : 3; }
@@ -707,7 +767,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
     const int slots = gridDim.x, slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
     Start st;
     unsigned per;
-    find_start<kNarrowRows, kNarrowStep, kNarrowWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
+    find_start<kNarrowRows, kNarrowStep, kNarrowExtra, kNarrowWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
     unsigned line = (unsigned)slot * per;
     const unsigned end = min(line + per, (unsigned)st.all * (unsigned)a.kv_heads);
     Meta *meta = reinterpret_cast<Meta *>(a.meta) + slot;
@@ -727,20 +787,23 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             u.first = __builtin_amdgcn_readfirstlane(u.first);
             u.n = __builtin_amdgcn_readfirstlane(u.n);
             u.len = __builtin_amdgcn_readfirstlane(u.len);
-            span<kNarrowRows, kNarrowStep>(a, u);
-            const int take = (int)min((unsigned)(u.steps - into), end - line);
+            span<kNarrowRows, kNarrowStep, kNarrowExtra>(a, u);
+            // [into, into + here) of the unit's place on the line: steps from .. to, if any
+            const int here = (int)min((unsigned)(u.cost - into), end - line);
+            const int from = max(into - kNarrowExtra, 0), take = into + here - kNarrowExtra - from;
+            if (take > 0) {
             const int row0 = u.tile * kNarrowRows, nrows = min(u.n * a.group - row0, kNarrowRows);
 
             // all rows see keys from some_lo on up to some_hi; any row, those from kbeg on up to kend
             int some_lo = 0, some_hi;
             {
-                const int p0 = u.len - u.n + row0 / a.group, p1 = u.len - u.n + (row0 + nrows - 1) / a.group;
+                const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, row0 + nrows - 1);
                 some_hi = max(min(u.kend, p0 + 1), 0);
                 if (a.window)
                     some_lo = max(p1 - a.window + 1, 0);
             }
-            const int hi = min((u.s0 + into + take) * kNarrowStep, u.kend);
-            int blk = (u.s0 + into) * kNarrowWaves + wave;
+            const int hi = min((u.s0 + from + take) * kNarrowStep, u.kend);
+            int blk = (u.s0 + from) * kNarrowWaves + wave;
             while ((blk + 1) * kBlk <= u.kbeg)
                 blk += kNarrowWaves;
             // the 16 keys from `key` on: their page's address, or 0 and a set bit in `gone`
@@ -836,7 +899,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             for (int d = 0; d < R::kO; ++d)
                 *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[0][d] * f;
             __syncthreads();
-            const bool begins = into == 0, ends = into + take == u.steps;
+            const bool begins = from == 0, ends = from + take == u.steps;
             for (int x = tid; x < kNarrowRows * D / 4; x += kNarrowWaves * 64) {
                 const int r = x / (D / 4), ch = x % (D / 4);
                 float best = m_s[0][r];
@@ -865,12 +928,13 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 }
             }
             if (begins && !ends) {
-                // its last step is step line + steps - 1 of the line
-                parts = (int)((line + (unsigned)u.steps - 1u) / per) - slot + 1;
+                // the unit's last place on the line is line - into + cost - 1
+                parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
                 if (tid == 0)
                     *meta = Meta{parts, head, u.first, u.n * a.group, row0, {}};
             }
-            line += take;
+            }
+            line += here;
             if (line >= end)
                 break;
             // the next unit
@@ -899,6 +963,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 // operand that is read from LDS enters NT instructions: at two, reading takes as long as multiplying (128
 // bytes a cycle for four SIMDs' 32 cycles per KB).
 constexpr int kWideStep = 64;
+constexpr int kWideExtra = 1;
 constexpr int kWideWaves = 8;
 constexpr int wide_tiles(bool exact) { return exact ? 1 : 2; }
 constexpr int wide_rows(bool exact) { return kWideWaves * wide_tiles(exact) * 16; }
@@ -922,7 +987,7 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
         strange_s = 0;
     Start st;
     unsigned per;
-    find_start<kRows, kWideStep, kWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
+    find_start<kRows, kWideStep, kWideExtra, kWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
     unsigned line = (unsigned)slot * per;
     const unsigned end = min(line + per, (unsigned)st.all * (unsigned)a.kv_heads);
     Meta *meta = reinterpret_cast<Meta *>(a.meta) + slot;
@@ -941,8 +1006,11 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             u.first = __builtin_amdgcn_readfirstlane(u.first);
             u.n = __builtin_amdgcn_readfirstlane(u.n);
             u.len = __builtin_amdgcn_readfirstlane(u.len);
-            span<kRows, kWideStep>(a, u);
-            const int take = (int)min((unsigned)(u.steps - into), end - line);
+            span<kRows, kWideStep, kWideExtra>(a, u);
+            // [into, into + here) of the unit's place on the line: steps from .. to, if any
+            const int here = (int)min((unsigned)(u.cost - into), end - line);
+            const int from = max(into - kWideExtra, 0), take = into + here - kWideExtra - from;
+            if (take > 0) {
             const int unit0 = u.tile * kRows, nrows = min(u.n * a.group - unit0, kRows);
             const int row0 = unit0 + wave * kTiles * 16;
             const bool active = row0 < unit0 + nrows;   // the wave has rows
@@ -950,7 +1018,7 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             int some_lo = 0, some_hi = 0, any_lo = 0, any_hi = 0;
             if (active) {
                 const int last = min(row0 + kTiles * 16, unit0 + nrows) - 1;
-                const int p0 = u.len - u.n + row0 / a.group, p1 = u.len - u.n + last / a.group;
+                const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, last);
                 some_hi = max(min(u.kend, p0 + 1), 0);
                 any_hi = max(min(u.kend, p1 + 1), 0);
                 if (a.window) {
@@ -958,10 +1026,10 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
                     any_lo = max(p0 - a.window + 1, 0);
                 }
             }
-            const int first = u.s0 + into;
+            const int first = u.s0 + from;
             // all rows of the unit see the keys from unit_lo on up to unit_hi
-            const int unit_hi = min(u.kend, u.len - u.n + unit0 / a.group + 1);
-            const int unit_lo = a.window ? u.len - u.n + (unit0 + nrows - 1) / a.group - a.window + 1 : 0;
+            const int unit_hi = min(u.kend, u.len - u.n + by_group(a, unit0) + 1);
+            const int unit_lo = a.window ? u.len - u.n + by_group(a, unit0 + nrows - 1) - a.window + 1 : 0;
             // The pages of a step's groups of 16 keys
             auto ids_of = [&](int step, int (&id)[kGroups]) {
 #pragma unroll
@@ -1040,7 +1108,7 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
                 }
             }
             rows.end();
-            const bool begins = into == 0, ends = into + take == u.steps;
+            const bool begins = from == 0, ends = from + take == u.steps;
             // Through LDS, a column tile at a time, so that whole rows are written. (Both buffers have been read; a wave
             // reads what its own lanes wrote.)
             float *mine = reinterpret_cast<float *>(wave < kWaves / 2 ? kbuf : vbuf) + wave % (kWaves / 2) * (16 * D);
@@ -1076,11 +1144,12 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             }
             __syncthreads();
             if (begins && !ends) {
-                parts = (int)((line + (unsigned)u.steps - 1u) / per) - slot + 1;
+                parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
                 if (tid == 0)
                     *meta = Meta{parts, head, u.first, u.n * a.group, unit0, {}};
             }
-            line += take;
+            }
+            line += here;
             if (line >= end)
                 break;
             into = 0;
@@ -1103,32 +1172,107 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
 }
 
 // ---- units that a border cut ---------------------------------------------------------
-// Workgroup (slot, y) joins 1024 / D rows of the unit that begins in the slot, if it ends in another:
-// o = sum_j 2^(c (m_j - m)) o_j and l likewise, over the parts in order.
-template <int ROWS, int D, class Q>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
+// o = sum_j 2^(c (m_j - m)) o_j and l likewise, over the parts in order, for the units that begin in a slot and end in
+// another.
+// Few rows, many parts: workgroup (slot, row). Its 256 threads are as many groups as hold a row at a time, and
+// a group takes every so many parts; their sums are added in the order of the groups.
+template <int D, class Q>
+__global__ __launch_bounds__(256) void attn_join_narrow_kernel(AttnArgs a)
 {
-    constexpr int kRows = 1024 / D, kLanes = D / 4;   // rows of a workgroup, threads of a row
-    const int slot = blockIdx.x, r = blockIdx.y * kRows + threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    constexpr int kLanes = D / 4, kGroups = 256 / kLanes, kMost = 768;
+    static_assert(narrow_per_cu(D) * 256 <= kMost, "as many parts as slots at most");
+    __shared__ float weight_s[kMost];
+    __shared__ v4f sum_s[256];
+    __shared__ float wave_s[2][4];
+    const int slot = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, group = tid / kLanes, d = tid % kLanes * 4;
     const Meta meta = reinterpret_cast<const Meta *>(a.meta)[slot];
     if (meta.parts == 0 || meta.row0 + r >= meta.rows)
         return;
-    const float *first = part_of<ROWS, D>(a, slot, true);
-    const float *others = part_of<ROWS, D>(a, slot + 1, false);
-    constexpr size_t kNext = 2 * ROWS * (D + 3);
-    const float c = first[ROWS * D + 2 * ROWS + r];
-    float best = first[ROWS * D + r];
-    for (int j = 1; j < meta.parts; ++j)
-        best = fmaxf(best, others[(j - 1) * kNext + ROWS * D + r]);
-    v4f o = {};
-    float l = 0.0f;
-    for (int j = 0; j < meta.parts; ++j) {
-        const float *p = j ? others + (j - 1) * kNext : first;
-        const float m = p[ROWS * D + r], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
-        o += *reinterpret_cast<const v4f *>(p + r * D + d) * f;
-        l += p[ROWS * D + ROWS + r] * f;
+    // part j, 0 of which is the slot's own
+    auto part = [&](int j) { return part_of<kNarrowRows, D>(a, slot + j, j == 0); };
+    constexpr int kM = kNarrowRows * D, kL = kM + kNarrowRows, kC = kL + kNarrowRows;
+    const float c = part(0)[kC + r];
+    float best = -INFINITY;
+    for (int j = tid; j < meta.parts; j += 256) {
+        weight_s[j] = part(j)[kM + r];
+        best = fmaxf(best, weight_s[j]);
     }
-    put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1)
+        best = fmaxf(best, __shfl_xor(best, x));
+    if ((tid & 63) == 0)
+        wave_s[0][tid >> 6] = best;
+    __syncthreads();
+    best = fmaxf(fmaxf(wave_s[0][0], wave_s[0][1]), fmaxf(wave_s[0][2], wave_s[0][3]));
+    float l = 0.0f;
+    for (int j = tid; j < meta.parts; j += 256) {
+        const float m = weight_s[j], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
+        weight_s[j] = f;
+        l += part(j)[kL + r] * f;
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1)
+        l += __shfl_xor(l, x);
+    if ((tid & 63) == 0)
+        wave_s[1][tid >> 6] = l;
+    __syncthreads();
+    l = (wave_s[1][0] + wave_s[1][1]) + (wave_s[1][2] + wave_s[1][3]);
+    v4f o = {};
+    constexpr int kAhead = 8;   // parts of a group whose loads are in flight
+    for (int j0 = group; j0 < meta.parts; j0 += kAhead * kGroups) {
+        v4f x[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int j = min(j0 + y * kGroups, meta.parts - 1);
+            x[y] = *reinterpret_cast<const v4f *>(part(j) + r * D + d);
+        }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int j = j0 + y * kGroups;
+            if (j < meta.parts)
+                o += x[y] * weight_s[j];
+        }
+    }
+    sum_s[tid] = o;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+        for (int x = 1; x < kGroups; ++x)
+            o += sum_s[x * kLanes + tid];
+        put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+    }
+}
+
+// Many rows, few parts: workgroup (slot, y) takes every kWideJoin-th 4 KB of the unit's rows.
+constexpr int kWideJoin = 16;
+
+template <int ROWS, int D, class Q>
+__global__ __launch_bounds__(256) void attn_join_wide_kernel(AttnArgs a)
+{
+    constexpr int kRows = 1024 / D, kLanes = D / 4;   // rows of a pass, threads of a row
+    const int slot = blockIdx.x, d = threadIdx.x % kLanes * 4;
+    const Meta meta = reinterpret_cast<const Meta *>(a.meta)[slot];
+    if (meta.parts == 0)
+        return;
+    auto part = [&](int j) { return part_of<ROWS, D>(a, slot + j, j == 0); };
+    constexpr int kM = ROWS * D, kL = kM + ROWS, kC = kL + ROWS;
+    const int end = min(ROWS, meta.rows - meta.row0);
+    for (int r = blockIdx.y * kRows + threadIdx.x / kLanes; r < end; r += kWideJoin * kRows) {
+        const float c = part(0)[kC + r];
+        float best = part(0)[kM + r];
+        for (int j = 1; j < meta.parts; ++j)
+            best = fmaxf(best, part(j)[kM + r]);
+        v4f o = {};
+        float l = 0.0f;
+#pragma unroll 2
+        for (int j = 0; j < meta.parts; ++j) {
+            const float *p = part(j);
+            const float m = p[kM + r], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
+            o += *reinterpret_cast<const v4f *>(p + r * D + d) * f;
+            l += p[kL + r] * f;
+        }
+        put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+    }
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -1160,9 +1304,9 @@ int launch(const AttnArgs &a, hipStream_t st)
         return TB_EHIP;
     constexpr int kRows = wide_rows(kExact);
     if (wide)
-        hipLaunchKernelGGL((attn_join_kernel<kRows, D, Q>), dim3(slots, kRows * D / 1024), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attn_join_wide_kernel<kRows, D, Q>), dim3(slots, kWideJoin), dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((attn_join_kernel<kNarrowRows, D, Q>), dim3(slots, kNarrowRows * D / 1024), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q>), dim3(slots, kNarrowRows), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
@@ -1220,7 +1364,7 @@ extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_k
     const long long limit = (long long)width * cache->page;
     // steps of all units are counted in 31 bits
     if (!can || limit > (1 << 30) ||
-        ((long long)tokens * q->heads / 16 + (long long)requests * cache->kv_heads) * (limit / 64 + 2) >= (1ll << 31))
+        ((long long)tokens * q->heads / 16 + (long long)requests * cache->kv_heads) * (limit / 64 + 4) >= (1ll << 31))
         return TB_EUNSUPPORTED;
     if (ws_bytes < need)
         return TB_EINVAL;
@@ -1231,7 +1375,11 @@ extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_k
     r.k = static_cast<const uint8_t *>(cache->k), r.v = static_cast<const uint8_t *>(cache->v);
     r.table = table, r.offsets = offsets, r.lengths = lengths;
     r.pages = cache->pages, r.page_shift = tbh::log2_of(cache->page), r.width = width, r.kv_heads = cache->kv_heads;
-    r.group = q->heads / cache->kv_heads, r.requests = requests, r.tokens = tokens;
+    r.group = q->heads / cache->kv_heads;
+    while ((1u << r.group_shift) < (uint32_t)r.group)
+        ++r.group_shift;
+    r.group_mul = (uint32_t)(((1ull << 32) * ((1ull << r.group_shift) - (uint64_t)r.group)) / (uint64_t)r.group + 1);
+    r.requests = requests, r.tokens = tokens;
     r.window = std::min(window, 1 << 30), r.scale = scale * kLog2e, r.out = out;
     r.meta = static_cast<int32_t *>(ws), r.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMetaBytes);
     const hipStream_t st = static_cast<hipStream_t>(stream);
