@@ -180,7 +180,8 @@ __device__ __forceinline__ int scan(int v, int *wave_s, int &total)
 
 struct Start {
     int all;             // cost of all units of a kv head
-    int req, tile, into; // the unit where the slot's stretch of the line begins, and the line's place in it
+    int req, into;       // the unit where the slot's stretch of the line begins, and the line's place in it
+    Unit u;
 };
 
 // A thread's walk along the tiles of the requests.
@@ -251,8 +252,9 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
                 break;
             st.into -= w.u.cost;
         }
-        st.tile = __builtin_amdgcn_readfirstlane(w.u.tile);
         st.into = __builtin_amdgcn_readfirstlane(st.into);
+        st.u = {__builtin_amdgcn_readfirstlane(w.u.first), __builtin_amdgcn_readfirstlane(w.u.n), __builtin_amdgcn_readfirstlane(w.u.len),
+                __builtin_amdgcn_readfirstlane(w.u.tile)};
         return;
     }
     constexpr int kThreads = WAVES * 64;
@@ -312,14 +314,16 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
             at += w.u.cost;
             w.next(a);
         }
-        found_s[0] = w.r;
-        found_s[1] = w.u.tile;
-        found_s[2] = want - at;
+        const int found[6] = {w.r, want - at, w.u.first, w.u.n, w.u.len, w.u.tile};
+#pragma unroll
+        for (int x = 0; x < 6; ++x)
+            found_s[x] = found[x];
     }
     __syncthreads();
     st.req = __builtin_amdgcn_readfirstlane(found_s[0]);
-    st.tile = __builtin_amdgcn_readfirstlane(found_s[1]);
-    st.into = __builtin_amdgcn_readfirstlane(found_s[2]);
+    st.into = __builtin_amdgcn_readfirstlane(found_s[1]);
+    st.u = {__builtin_amdgcn_readfirstlane(found_s[2]), __builtin_amdgcn_readfirstlane(found_s[3]), __builtin_amdgcn_readfirstlane(found_s[4]),
+            __builtin_amdgcn_readfirstlane(found_s[5])};
 }
 
 // ---- a wave's rows ------------------------------------------------------------------
@@ -421,18 +425,36 @@ struct Rows {
         return make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
 
-    // Rows row0 .. row0 + 16 NT - 1 of a unit (rows past the last are that one): their q, and what they see.
-    __device__ __forceinline__ void begin(const AttnArgs &a, const Unit &u, int head, int row0, int lane)
+    // Rows row0 .. row0 + 16 NT - 1 of a unit (rows past the last are that one): what they see, and their q, asked for
+    // here and made operands by begin().
+    struct Raw {
+        Eight<typename std::conditional<EXACT, float, T>::type> e[NT][kQ];
+    };
+    __device__ __forceinline__ void fetch(const AttnArgs &a, const Unit &u, int head, int row0, int lane, Raw &raw)
     {
+        using E = typename std::conditional<EXACT, float, T>::type;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = min(row0 + 16 * n + (lane & 15), u.n * a.group - 1), tok = by_group(a, r), h = head * a.group + r - tok * a.group;
             pos[n] = u.len - u.n + tok;
-            load_q(a, n, (size_t)((long long)(u.first + tok) * a.q_row + (long long)h * a.q_head) + 8 * (lane >> 4));
+            const E *at = static_cast<const E *>(a.q) + (long long)(u.first + tok) * a.q_row + (long long)h * a.q_head + 8 * (lane >> 4);
+#pragma unroll
+            for (int s = 0; s < kQ; ++s)
+                raw.e[n][s].load(at + 32 * s);
         }
-        // loaded here, or the wait for these loads stands in the loop over the keys, where it would also be one for theirs
+    }
+    __device__ __forceinline__ void begin(const AttnArgs &a, Raw &raw)
+    {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            if constexpr (!EXACT) {
+#pragma unroll
+                for (int s = 0; s < kQ; ++s)
+                    q[n][s][0] = raw.e[n][s].w;
+            } else {
+                split_q(a, n, raw.e[n]);
+            }
+            // loaded here, or the wait for these loads stands in the loop over the keys, where it would also be one for theirs
 #pragma unroll
             for (int s = 0; s < kQ; ++s)
 #pragma unroll
@@ -445,55 +467,45 @@ struct Rows {
                 o[n][d] = v4f{};
         }
     }
-    __device__ __forceinline__ void load_q(const AttnArgs &a, int n, size_t at)
+    __device__ __forceinline__ void split_q(const AttnArgs &a, int n, Eight<float> (&e)[kQ])
     {
-        if constexpr (!EXACT) {
-#pragma unroll
-            for (int s = 0; s < kQ; ++s)
-                q[n][s][0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + at + 32 * s);
-        } else {
-            Eight<float> e[kQ];
-#pragma unroll
-            for (int s = 0; s < kQ; ++s)
-                e[s].load(static_cast<const float *>(a.q) + at + 32 * s);
-            if constexpr (std::is_same<T, F16>::value) {
-                // the row's largest element between 2^9 and 2^10: whatever the row's magnitude, its parts are fp16 numbers
-                float top = 0.0f, v[8];
-#pragma unroll
-                for (int s = 0; s < kQ; ++s) {
-                    e[s].get(v);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        top = fmaxf(top, fabsf(v[x]));
-                }
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const int ex = top > 0.0f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 1), 254) - 127 : 9;
-                // 2^(9 - ex) in two factors, either of which fp32 holds
-                const int half = (9 - ex) / 2;
-                const float f = __builtin_ldexpf(1.0f, half), f2 = __builtin_ldexpf(1.0f, 9 - ex - half);
-#pragma unroll
-                for (int s = 0; s < kQ; ++s) {
-                    e[s].get(v);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        v[x] = v[x] * f * f2;
-                    e[s].set(v);
-                }
-                factor[n] = a.scale / f / f2;
-            }
+        if constexpr (std::is_same<T, F16>::value) {
+            // the row's largest element between 2^9 and 2^10: whatever the row's magnitude, its parts are fp16 numbers
+            float top = 0.0f, v[8];
 #pragma unroll
             for (int s = 0; s < kQ; ++s) {
-                float v[8];
                 e[s].get(v);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t w[kParts];
-                    Split<T, EXACT>::pair(v[2 * x], v[2 * x + 1], w);
+                for (int x = 0; x < 8; ++x)
+                    top = fmaxf(top, fabsf(v[x]));
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const int ex = top > 0.0f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 1), 254) - 127 : 9;
+            // 2^(9 - ex) in two factors, either of which fp32 holds
+            const int half = (9 - ex) / 2;
+            const float f = __builtin_ldexpf(1.0f, half), f2 = __builtin_ldexpf(1.0f, 9 - ex - half);
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
-                        word(q[n][s][p], x) = w[p];
-                }
+            for (int s = 0; s < kQ; ++s) {
+                e[s].get(v);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    v[x] = v[x] * f * f2;
+                e[s].set(v);
+            }
+            factor[n] = a.scale / f / f2;
+        }
+#pragma unroll
+        for (int s = 0; s < kQ; ++s) {
+            float v[8];
+            e[s].get(v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t w[kParts];
+                Split<T, EXACT>::pair(v[2 * x], v[2 * x + 1], w);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    word(q[n][s][p], x) = w[p];
             }
         }
     }
@@ -760,7 +772,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
     __shared__ __align__(128) uint8_t kbuf[kNarrowWaves * kBuf];
     __shared__ __align__(128) uint8_t vbuf[kNarrowWaves * kBuf];
     __shared__ int chunk_s[kNarrowWaves * 64];
-    __shared__ int wave_s[kNarrowWaves], found_s[3];
+    __shared__ int wave_s[kNarrowWaves], found_s[6];
     __shared__ float m_s[kNarrowWaves][kNarrowRows], l_s[kNarrowWaves][kNarrowRows], c_s[kNarrowRows];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
     // neighbours on the line of units share keys: they go to the same XCD (workgroup b runs on XCD b % 8)
@@ -776,17 +788,12 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
         lds_t *kb = (lds_t *)kbuf + wave * kBuf, *vb = (lds_t *)vbuf + wave * kBuf;
         const const_ints table = (const_ints)a.table;
         int head = (int)(line / (unsigned)st.all), req = st.req, into = st.into;
-        Unit u;
-        u.tile = st.tile;
+        Unit u = st.u;
         Loader<D> loader;
         loader.init(lane);
         R rows;
         rows.init_reads(lane);
         for (;;) {
-            request_of(a, req, u.first, u.n, u.len);
-            u.first = __builtin_amdgcn_readfirstlane(u.first);
-            u.n = __builtin_amdgcn_readfirstlane(u.n);
-            u.len = __builtin_amdgcn_readfirstlane(u.len);
             span<kNarrowRows, kNarrowStep, kNarrowExtra>(a, u);
             // [into, into + here) of the unit's place on the line: steps from .. to, if any
             const int here = (int)min((unsigned)(u.cost - into), end - line);
@@ -806,46 +813,54 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             int blk = (u.s0 + from) * kNarrowWaves + wave;
             while ((blk + 1) * kBlk <= u.kbeg)
                 blk += kNarrowWaves;
-            // the 16 keys from `key` on: their page's address, or 0 and a set bit in `gone`
-            auto place = [&](int key, int t, uint32_t &gone) {
-                int id = -1;
-                if (key < u.kend)
-                    id = table[(size_t)req * a.width + (key >> a.page_shift)];
-                if ((unsigned)id >= (unsigned)a.pages) {
-                    gone |= 1u << t;
-                    id = 0;
-                }
-                return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
-            };
-            size_t at[2] = {0, 0};
-            uint32_t gone = 0;
-            if (blk * kBlk < hi) {
+            // The pages of a block's two groups of 16 keys, read a block ahead; then the groups' places. A group without a page
+            // is read from page 0, and not used.
+            auto ids_of = [&](int b, int (&id)[2]) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    at[t] = place(blk * kBlk + 16 * t, t, gone);
+                    id[t] = table[(size_t)req * a.width + (min(b * kBlk + 16 * t, u.kend - 1) >> a.page_shift)];
+            };
+            auto place = [&](int b, const int (&id)[2], size_t (&at)[2]) {
+                uint32_t gone = 0;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int key = b * kBlk + 16 * t;
+                    const bool page = (unsigned)id[t] < (unsigned)a.pages;
+                    gone |= page && key < u.kend ? 0u : 1u << t;
+                    at[t] = ((((size_t)(page ? id[t] : 0) * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
+                }
+                return gone;
+            };
+            int id[2] = {-1, -1};
+            const bool any = blk * kBlk < hi;
+            if (any)
+                ids_of(blk, id);
+            typename R::Raw raw;
+            rows.fetch(a, u, head, row0, opaque(lane), raw);
+            rows.begin(a, raw);
+            size_t at[2] = {0, 0};
+            uint32_t gone = 0;
+            if (any) {
+                gone = place(blk, id, at);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     loader.load(a.k + at[t], kb + t * 16 * D * 2);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     loader.load(a.v + at[t], vb + t * 16 * D * 2);
+                ids_of(blk + kNarrowWaves, id);
             }
-            rows.begin(a, u, head, row0, lane);   // behind the loads of keys and values: waited for once, with them
             while (blk * kBlk < hi) {
                 const int key0 = blk * kBlk, next = blk + kNarrowWaves;
                 const bool more = next * kBlk < hi;
                 size_t nat[2] = {0, 0};
                 uint32_t ngone = 0;
-                if (more) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        nat[t] = place(next * kBlk + 16 * t, t, ngone);
-                }
                 v4f s[1][2];
                 landed<2 * Loader<D>::kLoads>();   // all but the values, which were asked for last
                 rows.scores(kb, s);
                 lds_read();
                 if (more) {
+                    ngone = place(next, id, nat);
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         loader.load(a.k + nat[t], kb + t * 16 * D * 2);
@@ -875,6 +890,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         loader.load(a.v + nat[t], vb + t * 16 * D * 2);
+                    ids_of(next + kNarrowWaves, id);
                 }
                 gone = ngone;
                 at[0] = nat[0], at[1] = nat[1];
@@ -942,14 +958,17 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             ++u.tile;
             if (u.tile * kNarrowRows >= u.n * a.group) {
                 u.tile = 0;
-                int first, n, len;
                 do {
                     if (++req == a.requests) {
                         req = 0;
                         ++head;
                     }
-                    request_of(a, req, first, n, len);
-                } while (__builtin_amdgcn_readfirstlane(n) == 0);   // line < end: there is one
+                    int f, n, len;
+                    request_of(a, req, f, n, len);
+                    u.first = __builtin_amdgcn_readfirstlane(f);
+                    u.n = __builtin_amdgcn_readfirstlane(n);
+                    u.len = __builtin_amdgcn_readfirstlane(len);
+                } while (u.n == 0);   // line < end: there is one
             }
             __syncthreads();
         }
@@ -979,7 +998,7 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
     __shared__ __align__(128) uint8_t kbuf[2 * kBuf];
     __shared__ __align__(128) uint8_t vbuf[2 * kBuf];
     __shared__ int chunk_s[kWaves * 64];
-    __shared__ int wave_s[kWaves], found_s[3];
+    __shared__ int wave_s[kWaves], found_s[6];
     __shared__ unsigned long long strange_s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
     const int slots = gridDim.x, slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
@@ -995,17 +1014,12 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
     if (line < end) {
         const const_ints table = (const_ints)a.table;
         int head = (int)(line / (unsigned)st.all), req = st.req, into = st.into;
-        Unit u;
-        u.tile = st.tile;
+        Unit u = st.u;
         Loader<D> loader;
         loader.init(lane);
         R rows;
         rows.init_reads(lane);
         for (;;) {
-            request_of(a, req, u.first, u.n, u.len);
-            u.first = __builtin_amdgcn_readfirstlane(u.first);
-            u.n = __builtin_amdgcn_readfirstlane(u.n);
-            u.len = __builtin_amdgcn_readfirstlane(u.len);
             span<kRows, kWideStep, kWideExtra>(a, u);
             // [into, into + here) of the unit's place on the line: steps from .. to, if any
             const int here = (int)min((unsigned)(u.cost - into), end - line);
@@ -1034,8 +1048,7 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             auto ids_of = [&](int step, int (&id)[kGroups]) {
 #pragma unroll
                 for (int x = 0; x < kGroups; ++x) {
-                    const int key = step * kWideStep + 16 * x;
-                    id[x] = key < u.kend ? table[(size_t)req * a.width + (key >> a.page_shift)] : -1;
+                    id[x] = table[(size_t)req * a.width + (min(step * kWideStep + 16 * x, max(u.kend - 1, 0)) >> a.page_shift)];
                 }
             };
             auto at_of = [&](int id, int key) {
@@ -1051,10 +1064,12 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             };
             int id[kGroups], next_id[kGroups];
             ids_of(first, id);
+            typename R::Raw raw;
+            rows.fetch(a, u, head, row0, opaque(lane), raw);
             load(first, 0, id);
             if (take > 1)
                 ids_of(first + 1, next_id);
-            rows.begin(a, u, head, row0, opaque(lane));
+            rows.begin(a, raw);
             landed<0>();
             __syncthreads();
             for (int x = 0; x < take; ++x) {
@@ -1156,14 +1171,17 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             ++u.tile;
             if (u.tile * kRows >= u.n * a.group) {
                 u.tile = 0;
-                int f, n, len;
                 do {
                     if (++req == a.requests) {
                         req = 0;
                         ++head;
                     }
+                    int f, n, len;
                     request_of(a, req, f, n, len);
-                } while (__builtin_amdgcn_readfirstlane(n) == 0);   // line < end: there is one
+                    u.first = __builtin_amdgcn_readfirstlane(f);
+                    u.n = __builtin_amdgcn_readfirstlane(n);
+                    u.len = __builtin_amdgcn_readfirstlane(len);
+                } while (u.n == 0);   // line < end: there is one
             }
         }
     }
@@ -1174,16 +1192,18 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
 // ---- units that a border cut ---------------------------------------------------------
 // o = sum_j 2^(c (m_j - m)) o_j and l likewise, over the parts in order, for the units that begin in a slot and end in
 // another.
-// Few rows, many parts: workgroup (slot, row). Its 256 threads are as many groups as hold a row at a time, and
+// Few rows, many parts: workgroup (slot, row). Its threads are as many groups as hold a row at a time, and
 // a group takes every so many parts; their sums are added in the order of the groups.
+constexpr int kJoinThreads = 1024;
+
 template <int D, class Q>
-__global__ __launch_bounds__(256) void attn_join_narrow_kernel(AttnArgs a)
+__global__ __launch_bounds__(kJoinThreads) void attn_join_narrow_kernel(AttnArgs a)
 {
-    constexpr int kLanes = D / 4, kGroups = 256 / kLanes, kMost = 768;
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kWaves = kJoinThreads / 64, kMost = 768;
     static_assert(narrow_per_cu(D) * 256 <= kMost, "as many parts as slots at most");
     __shared__ float weight_s[kMost];
-    __shared__ v4f sum_s[256];
-    __shared__ float wave_s[2][4];
+    __shared__ v4f sum_s[kJoinThreads];
+    __shared__ float wave_s[2][kWaves];
     const int slot = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, group = tid / kLanes, d = tid % kLanes * 4;
     const Meta meta = reinterpret_cast<const Meta *>(a.meta)[slot];
     if (meta.parts == 0 || meta.row0 + r >= meta.rows)
@@ -1193,7 +1213,7 @@ __global__ __launch_bounds__(256) void attn_join_narrow_kernel(AttnArgs a)
     constexpr int kM = kNarrowRows * D, kL = kM + kNarrowRows, kC = kL + kNarrowRows;
     const float c = part(0)[kC + r];
     float best = -INFINITY;
-    for (int j = tid; j < meta.parts; j += 256) {
+    for (int j = tid; j < meta.parts; j += kJoinThreads) {
         weight_s[j] = part(j)[kM + r];
         best = fmaxf(best, weight_s[j]);
     }
@@ -1203,9 +1223,11 @@ __global__ __launch_bounds__(256) void attn_join_narrow_kernel(AttnArgs a)
     if ((tid & 63) == 0)
         wave_s[0][tid >> 6] = best;
     __syncthreads();
-    best = fmaxf(fmaxf(wave_s[0][0], wave_s[0][1]), fmaxf(wave_s[0][2], wave_s[0][3]));
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x)
+        best = fmaxf(best, wave_s[0][x]);
     float l = 0.0f;
-    for (int j = tid; j < meta.parts; j += 256) {
+    for (int j = tid; j < meta.parts; j += kJoinThreads) {
         const float m = weight_s[j], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
         weight_s[j] = f;
         l += part(j)[kL + r] * f;
@@ -1216,7 +1238,10 @@ __global__ __launch_bounds__(256) void attn_join_narrow_kernel(AttnArgs a)
     if ((tid & 63) == 0)
         wave_s[1][tid >> 6] = l;
     __syncthreads();
-    l = (wave_s[1][0] + wave_s[1][1]) + (wave_s[1][2] + wave_s[1][3]);
+    l = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x)
+        l += wave_s[1][x];
     v4f o = {};
     constexpr int kAhead = 8;   // parts of a group whose loads are in flight
     for (int j0 = group; j0 < meta.parts; j0 += kAhead * kGroups) {
@@ -1306,7 +1331,7 @@ int launch(const AttnArgs &a, hipStream_t st)
     if (wide)
         hipLaunchKernelGGL((attn_join_wide_kernel<kRows, D, Q>), dim3(slots, kWideJoin), dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q>), dim3(slots, kNarrowRows), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q>), dim3(slots, kNarrowRows), dim3(kJoinThreads), 0, st, a);
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
