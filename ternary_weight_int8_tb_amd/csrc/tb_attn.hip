@@ -327,13 +327,20 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
 }
 
 // ---- a wave's rows ------------------------------------------------------------------
-// 32-byte segment c of row r of K or V lies at segment c ^ fold(r) of the row, so that neither the reads of K
-// (16 rows of 16 bytes) nor those of V (16 rows of 32 bytes) meet in the same banks.
+// Where 16 rows of K or V lie in LDS, so that neither the reads of K (16 rows of 16 bytes, 8 lanes a cycle) nor those of V
+// (16 rows of 32 bytes) meet in the same banks (64 of 4 bytes).
+//   D = 256: rows r and r + 8 side by side, which one load fills, and 32 bytes between such pairs: all places of a lane
+//   are one register and constants.
+//   Else four or eight rows side by side, and segment c of 32 bytes of row r at segment c ^ fold(r) of 8 or 4.
 template <int D>
-__device__ __forceinline__ int fold(int row)
-{
-    return D >= 128 ? row & 7 : (row >> 1) & 3;
-}
+struct Lay {
+    static constexpr bool kApart = D == 256;
+    static constexpr int kPair = 1024 + 32, kGroup = kApart ? 8 * kPair : 16 * D * 2;
+    static constexpr int kSegs = D >= 128 ? 8 : 4;                  // that fold turns
+    static constexpr int kKinds = kApart ? 1 : kSegs;               // registers for a lane's places in V, and twice those in K
+    static __device__ __forceinline__ int fold(int row) { return kApart ? 0 : D == 128 ? row & 7 : (row >> 1) & 3; }
+    static __device__ __forceinline__ int row(int r) { return kApart ? (r & 7) * kPair + (r >> 3) * 512 : r * D * 2; }
+};
 
 // The same in all lanes, in scalar registers
 __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
@@ -346,13 +353,14 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
 // 16 keys, one contiguous stretch of a page, to LDS
 template <int D>
 struct Loader {
+    using L = Lay<D>;
     static constexpr int kLoads = D / 32;    // of 1 KB
-    uint32_t off;                            // of the lane's 16 bytes in a load, at their places in LDS
+    uint32_t off;                            // of the lane's 16 bytes in a load
     __device__ __forceinline__ void init(int lane)
     {
         constexpr int kLanes = D / 8;   // of a row
         const int row = lane / kLanes, c = lane % kLanes;
-        off = (uint32_t)(row * D * 2 + (((c >> 1) ^ fold<D>(row)) << 5) + (c & 1) * 16);
+        off = L::kApart ? (uint32_t)(row * 8 * 512 + c * 16) : (uint32_t)(row * D * 2 + (((c >> 1) ^ L::fold(row)) << 5) + (c & 1) * 16);
     }
     __device__ __forceinline__ void pin() { asm volatile("" : "+v"(off)); }   // as Rows::pin_reads
     // `from` and `to` are the same in all lanes; lane l's 16 bytes go to to + 16 l. The compiler knows of the load's
@@ -365,10 +373,10 @@ struct Loader {
         const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)to);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            // rows 64 / kLanes * i on: their fold differs from row 0's in these bits alone
-            const uint32_t turn = (uint32_t)fold<D>(i * (512 / D)) << 5;
+            // rows i and i + 8; or the next four or eight, whose fold differs from the first ones' in these bits alone
+            const uint32_t turn = L::kApart ? 0u : (uint32_t)L::fold(i * (512 / D)) << 5;
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                         ::"s"(lds + i * 1024), "v"(off ^ turn), "s"(from + i * 1024)
+                         ::"s"(lds + i * (L::kApart ? L::kPair : 1024)), "v"(off ^ turn), "s"(from + i * (L::kApart ? 512 : 1024))
                          : "memory");   // m0 is the compiler's to set, and it sets it wherever it needs it
         }
     }
@@ -393,7 +401,9 @@ struct Rows {
     v4f o[NT][kO];
     float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
     int pos[NT];                      // the row's position: it sees the keys up to it
-    uint32_t kread, vread;            // the lane's places in a row of K, and of V
+    using L = Lay<D>;
+    static constexpr int kKk = L::kApart ? 1 : L::kKinds / 2;
+    uint32_t kread[kKk], vread[L::kKinds];   // the lane's places in a row of K, and of V
 
     // one factor for all rows, unless they have been scaled
     static constexpr bool kScaled = EXACT && std::is_same<T, F16>::value;
@@ -402,26 +412,27 @@ struct Rows {
     __device__ __forceinline__ void init_reads(int lane)
     {
         const int i = lane & 15, g = lane >> 4, row = 4 * g + (i >> 2);
-        kread = (uint32_t)(i * D * 2 + (((g >> 1) ^ fold<D>(i)) << 5) + (g & 1) * 16);
-        vread = (uint32_t)(row * D * 2 + (fold<D>(row) << 5) + (i & 3) * 8);
+#pragma unroll
+        for (int x = 0; x < kKk; ++x)
+            kread[x] = (uint32_t)(L::row(i) + (((2 * x + (g >> 1)) ^ L::fold(i)) << 5) + (g & 1) * 16);
+#pragma unroll
+        for (int x = 0; x < L::kKinds; ++x)
+            vread[x] = (uint32_t)(L::row(row) + ((x ^ L::fold(row)) << 5) + (i & 3) * 8);
     }
-    // Called in the loop over the keys: keeps every place that the reads of a step derive from these two from being
-    // kept in registers of its own
-    __device__ __forceinline__ void pin_reads() { asm volatile("" : "+v"(kread), "+v"(vread)); }
-    // Segments within 256 (or 128) bytes are turned by fold, those beyond stand apart
-    static constexpr int kSegs = D >= 128 ? 8 : 4;
+    // 16 keys' elements 32 s + 8 g .. + 7 of group t
     __device__ __forceinline__ uint4 key(const lds_t *buf, int t, int s) const
     {
-        const uint32_t at = (kread ^ (uint32_t)(2 * s % kSegs) << 5) + 2 * s / kSegs * 256;
-        return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) v4u *)(buf + at + t * 16 * D * 2));
+        const uint32_t at = kread[s % kKk] + s / kKk * (L::kApart ? 64 : L::kSegs * 32);
+        return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) v4u *)(buf + at + t * L::kGroup));
     }
+    // elements 16 d + lane % 16 of keys 4 g .. + 3 of both groups
     __device__ __forceinline__ uint4 value(const lds_t *buf, int d) const
     {
-        const uint32_t at = (vread ^ (uint32_t)(d % kSegs) << 5) + d / kSegs * 256;
+        const uint32_t at = vread[d % L::kKinds] + d / L::kKinds * (L::kApart ? 32 : L::kSegs * 32);
         uint2 w[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            w[t] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(buf + at + t * 16 * D * 2)));
+            w[t] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(buf + at + t * L::kGroup)));
         return make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
     }
 
@@ -542,16 +553,27 @@ struct Rows {
     }
     // Does row n see key k? (Keys from a unit's kend on are seen by none: their values are zeros, and see hide().)
     __device__ __forceinline__ bool sees(const AttnArgs &a, int n, int k) const { return k <= pos[n] && (!a.window || k > pos[n] - a.window); }
-    // `there`: bit x set where key x of the 32 is one that some row of the unit sees
-    __device__ __forceinline__ void hide(const AttnArgs &a, int key0, int g, uint32_t there, v4f (&s)[NT][2]) const
+    // Scores of keys that a row does not see. `there`: bit x set where key x of the 32 is one that some row of the unit sees.
+    // (A mask of the lane's eight keys for each tile of rows, and fences: the loop over the keys has no registers to spare.)
+    __device__ __forceinline__ void hide(const AttnArgs &a, int key0, int lane, uint32_t there, v4f (&s)[NT][2]) const
     {
+        const int first = lane >> 4 << 2;
+        there >>= first;
+        auto up_to = [](int keys) {   // the lane's keys below `keys`, counted from its first
+            return (1u << min(max(keys, 0), 4)) - 1u | ((1u << min(max(keys - 16, 0), 4)) - 1u) << 16;
+        };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int x = (j >> 2) * 16 + 4 * g + (j & 3);
+        for (int n = 0; n < NT; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int last = pos[n] - key0 - first;
+            uint32_t mask = there & up_to(last + 1);
+            if (a.window)
+                mask &= ~up_to(last - a.window + 1);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                s[n][j >> 2][j & 3] = (there >> x & 1) && sees(a, n, key0 + x) ? s[n][j >> 2][j & 3] : -INFINITY;
+            for (int j = 0; j < 8; ++j)
+                s[n][j >> 2][j & 3] = mask >> ((j >> 2) * 16 + (j & 3)) & 1 ? s[n][j >> 2][j & 3] : -INFINITY;
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     // The weights of 32 keys, and what they do to the maximum and the sum. The maximum follows only when a score
     // exceeds it by kLag: until then weights are larger than one, which costs no bits, and o stays as it is.
@@ -583,6 +605,7 @@ struct Rows {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            __builtin_amdgcn_sched_barrier(0);   // a tile's weights at a time
             const float base = m[n] == -INFINITY ? 0.0f : m[n];   // no key yet: all weights are 0
             float w[8];
 #pragma unroll
@@ -631,20 +654,24 @@ struct Rows {
     // place, as a weight of 0 would not keep them from the other rows.
     __device__ __forceinline__ void poison(const AttnArgs &a, int k, const uint8_t *v, int lane)
     {
-        v += 8 * (lane >> 4);
+        v = uniform(v);
+        uint32_t off = 8 * (lane >> 4);
 #pragma unroll
         for (int d = 0; d < kO; ++d) {
-            asm volatile("" : "+v"(v)::"memory");   // one load at a time: the loop over the keys has no registers to spare
-            const uint2 two = *reinterpret_cast<const uint2 *>(v + 32 * d);
-            float e[4];
-            unpack(two.x, e[0], e[1], T());
-            unpack(two.y, e[2], e[3], T());
+            asm volatile("" : "+v"(off)::"memory");   // one load at a time, see hide()
+            __builtin_amdgcn_sched_barrier(0);
+            const uint2 two = *reinterpret_cast<const uint2 *>(v + 32 * d + off);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                unpack(i < 2 ? two.x : two.y, lo, hi, T());
+                const float e = i & 1 ? hi : lo, odd = fabsf(e) < INFINITY ? 0.0f : e;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[n][d][i] += sees(a, n, k) && !(fabsf(e[i]) < INFINITY) ? e[i] : 0.0f;
+                for (int n = 0; n < NT; ++n)
+                    o[n][d][i] += sees(a, n, k) ? odd : 0.0f;
+            }
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     // the rows' sums, in all four lanes that share one
     __device__ __forceinline__ void end()
@@ -670,7 +697,7 @@ __device__ __forceinline__ uint64_t clean(lds_t *buf, uint64_t there, int me)
 #pragma unroll 1
     for (int pass = 0; pass < kPasses; ++pass) {
         const int x = pass * (LANES / kLanes) + me / kLanes;
-        __attribute__((address_space(3))) v4u *at = (__attribute__((address_space(3))) v4u *)(buf + x * D * 2 + me % kLanes * 16);
+        __attribute__((address_space(3))) v4u *at = (__attribute__((address_space(3))) v4u *)(buf + (x >> 4) * Lay<D>::kGroup + Lay<D>::row(x & 15) + me % kLanes * 16);
         v4u v = *at;
         const bool seen = there >> x & 1;
         bool odd = false;
@@ -767,7 +794,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
     using R = Rows<D, T, kExact, 1>;
-    constexpr int kBuf = kBlk * D * 2;
+    constexpr int kGroup = Lay<D>::kGroup, kBuf = 2 * kGroup;
     // arrays of their own: a read of one then waits for no load of the other
     __shared__ __align__(128) uint8_t kbuf[kNarrowWaves * kBuf];
     __shared__ __align__(128) uint8_t vbuf[kNarrowWaves * kBuf];
@@ -844,10 +871,10 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 gone = place(blk, id, at);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    loader.load(a.k + at[t], kb + t * 16 * D * 2);
+                    loader.load(a.k + at[t], kb + t * kGroup);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    loader.load(a.v + at[t], vb + t * 16 * D * 2);
+                    loader.load(a.v + at[t], vb + t * kGroup);
                 ids_of(blk + kNarrowWaves, id);
             }
             while (blk * kBlk < hi) {
@@ -863,12 +890,12 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                     ngone = place(next, id, nat);
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        loader.load(a.k + nat[t], kb + t * 16 * D * 2);
+                        loader.load(a.k + nat[t], kb + t * kGroup);
                 }
                 const bool whole = key0 >= some_lo && key0 + kBlk <= some_hi && !gone;
                 const uint32_t there = (uint32_t)key_bits(u.kbeg, u.kend, key0) & ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
                 if (!whole)
-                    rows.hide(a, key0, g, there, s);
+                    rows.hide(a, key0, lane, there, s);
                 uint4 p[1][R::kParts];
                 rows.weigh(a, s, p);
                 if (more)   // the next keys may be on their way
@@ -889,7 +916,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 if (more) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        loader.load(a.v + nat[t], vb + t * 16 * D * 2);
+                        loader.load(a.v + nat[t], vb + t * kGroup);
                     ids_of(next + kNarrowWaves, id);
                 }
                 gone = ngone;
@@ -910,7 +937,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             for (int w = 1; w < kNarrowWaves; ++w)
                 top = fmaxf(top, m_s[w][i]);
             const float f = rows.m[0] == top ? 1.0f : __builtin_amdgcn_exp2f((rows.m[0] - top) * rows.c(a, 0));
-            float *mine = reinterpret_cast<float *>(kbuf) + wave * kNarrowRows * D;
+            float *mine = reinterpret_cast<float *>(kbuf + wave * kBuf);
 #pragma unroll
             for (int d = 0; d < R::kO; ++d)
                 *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[0][d] * f;
@@ -926,7 +953,7 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 float l = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kNarrowWaves; ++w) {
-                    o += *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(kbuf) + (w * kNarrowRows + r) * D + (ch ^ r) * 4);
+                    o += *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(kbuf + w * kBuf) + r * D + (ch ^ r) * 4);
                     const float mw = m_s[w][r];
                     l += l_s[w][r] * (mw == best ? 1.0f : __builtin_amdgcn_exp2f((mw - best) * c_s[r]));
                 }
@@ -994,13 +1021,13 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
     constexpr bool kExact = std::is_same<Q, float>::value;
     constexpr int kWaves = kWideWaves, kTiles = wide_tiles(kExact), kRows = wide_rows(kExact);
     using R = Rows<D, T, kExact, kTiles>;
-    constexpr int kGroup = 16 * D * 2, kBuf = kWideStep * D * 2, kGroups = kWideStep / 16;
+    constexpr int kGroup = Lay<D>::kGroup, kGroups = kWideStep / 16, kBuf = kGroups * kGroup;
     __shared__ __align__(128) uint8_t kbuf[2 * kBuf];
     __shared__ __align__(128) uint8_t vbuf[2 * kBuf];
     __shared__ int chunk_s[kWaves * 64];
     __shared__ int wave_s[kWaves], found_s[6];
     __shared__ unsigned long long strange_s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slots = gridDim.x, slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
     if (tid == 0)
         strange_s = 0;
@@ -1097,15 +1124,14 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
                     const lds_t *kb = (const lds_t *)kbuf + b * kBuf + y * 2 * kGroup, *vb = (const lds_t *)vbuf + b * kBuf + y * 2 * kGroup;
                     const uint32_t mine = (uint32_t)(there >> (32 * y));
                     v4f s[kTiles][2];
-                    rows.pin_reads();
                     rows.scores(kb, s);
                     if (key0 < some_lo || key0 + kBlk > some_hi || ~mine)
-                        rows.hide(a, key0, g, mine, s);
+                        rows.hide(a, key0, opaque(lane), mine, s);
                     uint4 p[kTiles][R::kParts];
                     rows.weigh(a, s, p);
                     for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
                         const int z = __builtin_ctz(odd), group = 2 * y + (z >> 4);
-                        rows.poison(a, key0 + z, a.v + at_of(group == 0 ? id[0] : group == 1 ? id[1] : group == 2 ? id[2] : id[3], key0 + z), lane);
+                        rows.poison(a, key0 + z, a.v + at_of(group == 0 ? id[0] : group == 1 ? id[1] : group == 2 ? id[2] : id[3], key0 + z), opaque(lane));
                     }
                     rows.add(vb, p);
                 }
