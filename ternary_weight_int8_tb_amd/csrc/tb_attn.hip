@@ -1008,18 +1008,17 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 // 64 keys and their values at a time, in one of two buffers while the other is filled. With NT column tiles each
 // operand that is read from LDS enters NT instructions: at two, reading takes as long as multiplying (128
 // bytes a cycle for four SIMDs' 32 cycles per KB).
-constexpr int kWideStep = 64;
-constexpr int kWideExtra = 1;
-constexpr int kWideWaves = 8;
+constexpr int kWideStep = 64, kWideExtra = 2;
+constexpr int wide_waves(int dim) { return dim == 256 ? 8 : 4; }
 constexpr int wide_tiles(bool exact) { return exact ? 1 : 2; }
-constexpr int wide_rows(bool exact) { return kWideWaves * wide_tiles(exact) * 16; }
-constexpr int wide_per_cu(int dim, bool exact) { return dim == 64 && !exact ? 2 : 1; }
+constexpr int wide_rows(int dim, bool exact) { return wide_waves(dim) * wide_tiles(exact) * 16; }
+constexpr int wide_per_cu(int dim) { return dim == 256 ? 1 : dim == 128 ? 2 : 4; }   // workgroups
 
 template <int D, class T, class Q>
-__global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q, float>::value)) void attn_wide_kernel(AttnArgs a)
+__global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu(D)) void attn_wide_kernel(AttnArgs a)
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
-    constexpr int kWaves = kWideWaves, kTiles = wide_tiles(kExact), kRows = wide_rows(kExact);
+    constexpr int kWaves = wide_waves(D), kTiles = wide_tiles(kExact), kRows = wide_rows(D, kExact);
     using R = Rows<D, T, kExact, kTiles>;
     constexpr int kGroup = Lay<D>::kGroup, kGroups = kWideStep / 16, kBuf = kGroups * kGroup;
     __shared__ __align__(128) uint8_t kbuf[2 * kBuf];
@@ -1071,41 +1070,49 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
             // all rows of the unit see the keys from unit_lo on up to unit_hi
             const int unit_hi = min(u.kend, u.len - u.n + by_group(a, unit0) + 1);
             const int unit_lo = a.window ? u.len - u.n + by_group(a, unit0 + nrows - 1) - a.window + 1 : 0;
-            // The pages of a step's groups of 16 keys
-            auto ids_of = [&](int step, int (&id)[kGroups]) {
-#pragma unroll
-                for (int x = 0; x < kGroups; ++x) {
-                    id[x] = table[(size_t)req * a.width + (min(step * kWideStep + 16 * x, max(u.kend - 1, 0)) >> a.page_shift)];
-                }
-            };
+            // Of a step: group x of 16 keys; its page, if it has one; and the place of a key in the cache's arrays
+            auto id_of = [&](int key) { return table[(size_t)req * a.width + (min(key, max(u.kend - 1, 0)) >> a.page_shift)]; };
             auto at_of = [&](int id, int key) {
                 id = (unsigned)id < (unsigned)a.pages ? id : 0;
                 return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
             };
-            // wave 2 x loads the keys of group x, wave 2 x + 1 its values
-            static_assert(2 * kGroups == kWaves, "a group's keys or values per wave");
-            auto load = [&](int step, int b, const int (&id)[kGroups]) {
-                const int x = wave >> 1;
-                const size_t at = at_of(x == 0 ? id[0] : x == 1 ? id[1] : x == 2 ? id[2] : id[3], step * kWideStep + 16 * x);
-                loader.load((wave & 1 ? a.v : a.k) + at, (wave & 1 ? (lds_t *)vbuf : (lds_t *)kbuf) + b * kBuf + x * kGroup);
+            // The groups' keys and values are loaded by the waves in turn: items 2 x and 2 x + 1 are those of group x. A
+            // wave's pages are read a step ahead.
+            constexpr int kItems = 2 * kGroups / kWaves;
+            static_assert(kItems * kWaves == 2 * kGroups && kItems <= 2, "one item for each wave, or the keys and the values of a group");
+            const int mine16 = (wave * kItems >> 1) * 16;
+            auto load = [&](int step, int b, int id) {
+                const size_t at = at_of(id, step * kWideStep + mine16);
+                const int to = b * kBuf + (wave * kItems >> 1) * kGroup;
+                if (kItems == 2 || !(wave & 1))
+                    loader.load(a.k + at, (lds_t *)kbuf + to);
+                if (kItems == 2 || (wave & 1))
+                    loader.load(a.v + at, (lds_t *)vbuf + to);
             };
-            int id[kGroups], next_id[kGroups];
-            ids_of(first, id);
+            // keys of a step that some row sees
+            constexpr uint64_t kAll = ~0ull;
+            static_assert(kWideStep == 64, "a bit for each key");
+            auto there_of = [&](int step) {
+                uint64_t there = key_bits(u.kbeg, u.kend, step * kWideStep) & kAll;
+#pragma unroll
+                for (int x = 0; x < kGroups; ++x)
+                    there &= (unsigned)id_of(step * kWideStep + 16 * x) < (unsigned)a.pages ? ~0ull : ~(0xffffull << (16 * x));
+                return there;
+            };
+            int next_id = id_of(first * kWideStep + mine16);
             typename R::Raw raw;
             rows.fetch(a, u, head, row0, opaque(lane), raw);
-            load(first, 0, id);
-            if (take > 1)
-                ids_of(first + 1, next_id);
+            load(first, 0, next_id);
+            next_id = id_of((first + 1) * kWideStep + mine16);
+            uint64_t next_there = there_of(first);
             rows.begin(a, raw);
             landed<0>();
             __syncthreads();
             for (int x = 0; x < take; ++x) {
                 const int b = x & 1, step = first + x, step0 = step * kWideStep;
-                uint64_t there = key_bits(u.kbeg, u.kend, step0), strange = 0;
-#pragma unroll
-                for (int z = 0; z < kGroups; ++z)
-                    there &= (unsigned)id[z] < (unsigned)a.pages ? ~0ull : ~(0xffffull << (16 * z));
-                if (step0 < unit_lo || step0 + kWideStep > unit_hi || ~there) {
+                const uint64_t there = next_there;
+                uint64_t strange = 0;
+                if (step0 < unit_lo || step0 + kWideStep > unit_hi || there != kAll) {
                     const uint64_t odd = any_of(clean<D, T, kWaves * 64, kWideStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
                     if (odd && lane == 0)
                         atomicOr(&strange_s, (unsigned long long)odd);
@@ -1115,6 +1122,8 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
                 if (x + 1 < take) {
                     loader.pin();
                     load(step + 1, b ^ 1, next_id);
+                    next_id = id_of((step + 2) * kWideStep + mine16);
+                    next_there = there_of(step + 1);
                 }
 #pragma unroll 1
                 for (int y = 0; y < kWideStep / kBlk; ++y) {
@@ -1130,16 +1139,11 @@ __global__ __launch_bounds__(kWideWaves * 64, 2 * wide_per_cu(D, std::is_same<Q,
                     uint4 p[kTiles][R::kParts];
                     rows.weigh(a, s, p);
                     for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
-                        const int z = __builtin_ctz(odd), group = 2 * y + (z >> 4);
-                        rows.poison(a, key0 + z, a.v + at_of(group == 0 ? id[0] : group == 1 ? id[1] : group == 2 ? id[2] : id[3], key0 + z), opaque(lane));
+                        const int key = key0 + __builtin_ctz(odd);
+                        rows.poison(a, key, a.v + at_of(id_of(key), key), opaque(lane));
                     }
                     rows.add(vb, p);
                 }
-#pragma unroll
-                for (int z = 0; z < kGroups; ++z)
-                    id[z] = next_id[z];
-                if (x + 2 < take)
-                    ids_of(step + 2, next_id);
                 landed<0>();
                 __syncthreads();
                 if (strange) {
@@ -1294,36 +1298,48 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_narrow_kernel(AttnArgs
     }
 }
 
-// Many rows, few parts: workgroup (slot, y) takes every kWideJoin-th 4 KB of the unit's rows.
-constexpr int kWideJoin = 16;
-
+// Many rows, few parts: workgroup (slot, y) takes 4 KB of the unit's rows, four parts at a time.
 template <int ROWS, int D, class Q>
 __global__ __launch_bounds__(256) void attn_join_wide_kernel(AttnArgs a)
 {
-    constexpr int kRows = 1024 / D, kLanes = D / 4;   // rows of a pass, threads of a row
-    const int slot = blockIdx.x, d = threadIdx.x % kLanes * 4;
+    constexpr int kRows = 1024 / D, kLanes = D / 4, kAhead = 4;   // rows of the workgroup, threads of a row
+    const int slot = blockIdx.x, d = threadIdx.x % kLanes * 4, r = blockIdx.y * kRows + threadIdx.x / kLanes;
     const Meta meta = reinterpret_cast<const Meta *>(a.meta)[slot];
-    if (meta.parts == 0)
+    if (meta.parts == 0 || r >= ROWS || meta.row0 + r >= meta.rows)
         return;
     auto part = [&](int j) { return part_of<ROWS, D>(a, slot + j, j == 0); };
     constexpr int kM = ROWS * D, kL = kM + ROWS, kC = kL + ROWS;
-    const int end = min(ROWS, meta.rows - meta.row0);
-    for (int r = blockIdx.y * kRows + threadIdx.x / kLanes; r < end; r += kWideJoin * kRows) {
-        const float c = part(0)[kC + r];
-        float best = part(0)[kM + r];
-        for (int j = 1; j < meta.parts; ++j)
-            best = fmaxf(best, part(j)[kM + r]);
-        v4f o = {};
-        float l = 0.0f;
-#pragma unroll 2
-        for (int j = 0; j < meta.parts; ++j) {
-            const float *p = part(j);
-            const float m = p[kM + r], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
-            o += *reinterpret_cast<const v4f *>(p + r * D + d) * f;
-            l += p[kL + r] * f;
+    const float c = part(0)[kC + r];
+    float best = -INFINITY, l = 0.0f;
+    v4f o = {};
+    for (int j0 = 0; j0 < meta.parts; j0 += kAhead) {
+        v4f x[kAhead];
+        float m[kAhead], s[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const float *p = part(min(j0 + y, meta.parts - 1));
+            x[y] = *reinterpret_cast<const v4f *>(p + r * D + d);
+            m[y] = p[kM + r];
+            s[y] = p[kL + r];
         }
-        put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+        float now = best;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+            now = fmaxf(now, m[y]);
+        const float f = best == now ? 1.0f : __builtin_amdgcn_exp2f((best - now) * c);
+        o *= f;
+        l *= f;
+        best = now;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            if (j0 + y < meta.parts) {
+                const float g = m[y] == now ? 1.0f : __builtin_amdgcn_exp2f((m[y] - now) * c);
+                o += x[y] * g;
+                l += s[y] * g;
+            }
+        }
     }
+    put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -1332,13 +1348,13 @@ bool is_wide(int group, int requests, int tokens) { return (long long)tokens * g
 
 // As many workgroups as the chip's 256 CUs hold at a time: a constant, as the order of the sums must not depend
 // on a partition's size.
-int slots_of(bool wide, int dim, bool exact) { return 256 * (wide ? wide_per_cu(dim, exact) : narrow_per_cu(dim)); }
-constexpr size_t kMetaBytes = 768 * sizeof(Meta);
+int slots_of(bool wide, int dim) { return 256 * (wide ? wide_per_cu(dim) : narrow_per_cu(dim)); }
+constexpr size_t kMetaBytes = 1024 * sizeof(Meta);   // as many as slots at most
 
 size_t workspace(bool wide, int dim, bool exact)
 {
-    const int rows = wide ? wide_rows(exact) : kNarrowRows;
-    return kMetaBytes + (size_t)slots_of(wide, dim, exact) * 2 * rows * (dim + 3) * 4;
+    const int rows = wide ? wide_rows(dim, exact) : kNarrowRows;
+    return kMetaBytes + (size_t)slots_of(wide, dim) * 2 * rows * (dim + 3) * 4;
 }
 
 template <int D, class T, class Q>
@@ -1346,16 +1362,16 @@ int launch(const AttnArgs &a, hipStream_t st)
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
     const bool wide = is_wide(a.group, a.requests, a.tokens);
-    const int slots = slots_of(wide, D, kExact);
+    const int slots = slots_of(wide, D);
     if (wide)
-        hipLaunchKernelGGL((attn_wide_kernel<D, T, Q>), dim3(slots), dim3(kWideWaves * 64), 0, st, a);
+        hipLaunchKernelGGL((attn_wide_kernel<D, T, Q>), dim3(slots), dim3(wide_waves(D) * 64), 0, st, a);
     else
         hipLaunchKernelGGL((attn_narrow_kernel<D, T, Q>), dim3(slots), dim3(kNarrowWaves * 64), 0, st, a);
     if (hipGetLastError() != hipSuccess)
         return TB_EHIP;
-    constexpr int kRows = wide_rows(kExact);
+    constexpr int kRows = wide_rows(D, kExact);
     if (wide)
-        hipLaunchKernelGGL((attn_join_wide_kernel<kRows, D, Q>), dim3(slots, kWideJoin), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attn_join_wide_kernel<kRows, D, Q>), dim3(slots, kRows * D / 1024), dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q>), dim3(slots, kNarrowRows), dim3(kJoinThreads), 0, st, a);
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
