@@ -28,6 +28,7 @@ using namespace tbr;
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_t;
@@ -106,6 +107,16 @@ struct Split<F16, true> {
         w[1] = pack(a - ha, b - hb, F16());
     }
 };
+// The larger of two scores, in one operation: fmaxf first makes each operand, which the matrix instruction has written, a quiet
+// number, in one each, and the compiler makes fmaxf of a median whose third number it knows. (With a NaN the other, with two
+// infinity: such a row has no result anyway.)
+__device__ __forceinline__ float larger(float a, float b)
+{
+    float inf = INFINITY;
+    asm("" : "+s"(inf));
+    return __builtin_amdgcn_fmed3f(a, b, inf);
+}
+
 __device__ __forceinline__ uint32_t &word(uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // v, of which the compiler does not know that it is v: what is derived from it is derived where it is used, and not kept in
@@ -392,7 +403,9 @@ __device__ __forceinline__ void landed()
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // NT column tiles of 16 rows; lane l has, of each, row l % 16.
-template <int D, class T, bool EXACT, int NT>
+// AHEAD: operands of a block's first product are read together, and those of the second before the weights are made; else they
+// come a few at a time, for want of registers.
+template <int D, class T, bool EXACT, int NT, bool AHEAD>
 struct Rows {
     static constexpr int kQ = D / 32, kO = D / 16, kParts = Split<T, EXACT>::kParts;
     // fp16 weights start at 2^6: small ones keep their bits, and a row whose maximum lags by kLag still fits
@@ -401,6 +414,7 @@ struct Rows {
     v4f o[NT][kO];
     float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
     int pos[NT];                      // the row's position: it sees the keys up to it
+    bool small;                       // see weigh()
     using L = Lay<D>;
     static constexpr int kKk = L::kApart ? 1 : L::kKinds / 2;
     uint32_t kread[kKk], vread[L::kKinds];   // the lane's places in a row of K, and of V
@@ -456,6 +470,7 @@ struct Rows {
     }
     __device__ __forceinline__ void begin(const AttnArgs &a, Raw &raw)
     {
+        small = true;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if constexpr (!EXACT) {
@@ -525,12 +540,12 @@ struct Rows {
     // multiplied.
     __device__ __forceinline__ void scores(const lds_t *kb, v4f (&s)[NT][2]) const
     {
-        constexpr int kBatch = NT > 1 ? 2 : 4, kBatches = 2 * kQ / kBatch;
-        uint4 k[2][kBatch];
+        constexpr int kBatch = AHEAD ? 2 * kQ : NT > 1 ? 2 : 4, kBatches = 2 * kQ / kBatch;
+        uint4 k[AHEAD ? 1 : 2][kBatch];
         auto read = [&](int b) {
 #pragma unroll
             for (int x = 0; x < kBatch; ++x)
-                k[b & 1][x] = key(kb, x & 1, (b * kBatch + x) >> 1);
+                k[AHEAD ? 0 : b & 1][x] = key(kb, x & 1, (b * kBatch + x) >> 1);
         };
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -547,7 +562,7 @@ struct Rows {
                 for (int x = 0; x < kBatch; ++x)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        s[n][x & 1] = mfma(k[b & 1][x], q[n][(b * kBatch + x) >> 1][p], s[n][x & 1], T());
+                        s[n][x & 1] = mfma(k[AHEAD ? 0 : b & 1][x], q[n][(b * kBatch + x) >> 1][p], s[n][x & 1], T());
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -577,19 +592,21 @@ struct Rows {
     }
     // The weights of 32 keys, and what they do to the maximum and the sum. The maximum follows only when a score
     // exceeds it by kLag: until then weights are larger than one, which costs no bits, and o stays as it is.
-    // Scores are subtracted before they are scaled: one fused operation for both would leave the rounding of the
-    // maximum's product in the exponent, of any size where scores are large.
+    // One fused operation scales a score and takes the maximum's product from it, which leaves that product's rounding in all
+    // of a row's exponents: less than 2^-4 while it is `small`, below 2^20, and gone with the sum. Larger ones, and fp32
+    // rows, for which all weights would have to be that much more exact, are subtracted first.
     __device__ __forceinline__ void weigh(const AttnArgs &a, const v4f (&s)[NT][2], uint4 (&p)[NT][kParts])
     {
         float top[NT];
         bool more = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            top[n] = fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3]));
-            top[n] = fmaxf(top[n], fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+            top[n] = fmaxf(fmaxf(larger(s[n][0][0], s[n][0][1]), larger(s[n][0][2], s[n][0][3])),
+                           fmaxf(larger(s[n][1][0], s[n][1][1]), larger(s[n][1][2], s[n][1][3])));
             more |= (top[n] - m[n]) * c(a, n) > kLag;
         }
         if (__any(more)) {
+            bool fine = true;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
@@ -597,20 +614,32 @@ struct Rows {
                 const float now = fmaxf(m[n], top[n]);
                 const float f = now > m[n] ? __builtin_amdgcn_exp2f((m[n] - now) * c(a, n)) : 1.0f;
                 m[n] = now;
+                fine &= fabsf(now) * c(a, n) < 0x1p20f || now == -INFINITY;
                 l[n] *= f;
 #pragma unroll
                 for (int d = 0; d < kO; ++d)
                     o[n][d] *= f;
             }
+            small = __all(fine);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             __builtin_amdgcn_sched_barrier(0);   // a tile's weights at a time
             const float base = m[n] == -INFINITY ? 0.0f : m[n];   // no key yet: all weights are 0
             float w[8];
+            if (!EXACT && small) {
+                const float neg = __builtin_fmaf(-base, c(a, n), kBias);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = __builtin_fmaf(s[n][j >> 2][j & 3], c(a, n), neg);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = __builtin_fmaf(s[n][j >> 2][j & 3] - base, c(a, n), kBias);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3] - base, c(a, n), kBias));
+                w[j] = __builtin_amdgcn_exp2f(w[j]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t parts[kParts];
@@ -625,29 +654,51 @@ struct Rows {
             }
         }
     }
-    __device__ __forceinline__ void add(const lds_t *vb, const uint4 (&p)[NT][kParts])
+    struct Values {
+        uint4 v[AHEAD ? kO : 1];
+    };
+    __device__ __forceinline__ void read_ahead(const lds_t *vb, Values &w) const
     {
-        constexpr int kBatch = NT > 1 ? 2 : 4, kBatches = kO / kBatch;
-        uint4 v[2][kBatch];
-        auto read = [&](int b) {
+        if constexpr (AHEAD) {
 #pragma unroll
-            for (int x = 0; x < kBatch; ++x)
-                v[b & 1][x] = value(vb, b * kBatch + x);
-        };
-        read(0);
-#pragma unroll
-        for (int b = 0; b < kBatches; ++b) {
-            if (b + 1 < kBatches)
-                read(b + 1);
+            for (int d = 0; d < kO; ++d)
+                w.v[d] = value(vb, d);
             __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __device__ __forceinline__ void add(const lds_t *vb, const Values &w, const uint4 (&p)[NT][kParts])
+    {
+        if constexpr (AHEAD) {
 #pragma unroll
             for (int y = kParts; y-- > 0;)
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x)
+                for (int d = 0; d < kO; ++d)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        o[n][b * kBatch + x] = mfma(v[b & 1][x], p[n][y], o[n][b * kBatch + x], T());
-            __builtin_amdgcn_sched_barrier(0);
+                        o[n][d] = mfma(w.v[d], p[n][y], o[n][d], T());
+        } else {
+            constexpr int kBatch = NT > 1 ? 2 : 4, kBatches = kO / kBatch;
+            uint4 v[2][kBatch];
+            auto read = [&](int b) {
+#pragma unroll
+                for (int x = 0; x < kBatch; ++x)
+                    v[b & 1][x] = value(vb, b * kBatch + x);
+            };
+            read(0);
+#pragma unroll
+            for (int b = 0; b < kBatches; ++b) {
+                if (b + 1 < kBatches)
+                    read(b + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int y = kParts; y-- > 0;)
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            o[n][b * kBatch + x] = mfma(v[b & 1][x], p[n][y], o[n][b * kBatch + x], T());
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
     // The elements of key k's values (in memory at v) that are not finite, into the rows that see it: LDS holds zeros in their
@@ -660,7 +711,7 @@ struct Rows {
         for (int d = 0; d < kO; ++d) {
             asm volatile("" : "+v"(off)::"memory");   // one load at a time, see hide()
             __builtin_amdgcn_sched_barrier(0);
-            const uint2 two = *reinterpret_cast<const uint2 *>(v + 32 * d + off);
+            const uint2 two = __builtin_bit_cast(uint2, *(const __attribute__((address_space(1))) v2u *)(v + 32 * d + off));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float lo, hi;
@@ -793,7 +844,7 @@ template <int D, class T, class Q>
 __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narrow_kernel(AttnArgs a)
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
-    using R = Rows<D, T, kExact, 1>;
+    using R = Rows<D, T, kExact, 1, !kExact || D < 256>;
     constexpr int kGroup = Lay<D>::kGroup, kBuf = 2 * kGroup;
     // arrays of their own: a read of one then waits for no load of the other
     __shared__ __align__(128) uint8_t kbuf[kNarrowWaves * kBuf];
@@ -896,8 +947,6 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                 const uint32_t there = (uint32_t)key_bits(u.kbeg, u.kend, key0) & ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
                 if (!whole)
                     rows.hide(a, key0, lane, there, s);
-                uint4 p[1][R::kParts];
-                rows.weigh(a, s, p);
                 if (more)   // the next keys may be on their way
                     landed<2 * Loader<D>::kLoads>();
                 else
@@ -907,11 +956,15 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
                     strange = any_of(clean<D, T, 64, kBlk>(vb, there, lane));
                     lds_read();
                 }
+                typename R::Values values;
+                rows.read_ahead(vb, values);
+                uint4 p[1][R::kParts];
+                rows.weigh(a, s, p);
                 for (; strange; strange &= strange - 1) {
                     const int x = __builtin_ctzll(strange), t = x >> 4;
                     rows.poison(a, key0 + x, a.v + (t ? at[1] : at[0]) + (x & 15) * (D * 2), lane);
                 }
-                rows.add(vb, p);
+                rows.add(vb, values, p);
                 lds_read();
                 if (more) {
 #pragma unroll
@@ -1008,7 +1061,9 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 // 64 keys and their values at a time, in one of two buffers while the other is filled. With NT column tiles each
 // operand that is read from LDS enters NT instructions: at two, reading takes as long as multiplying (128
 // bytes a cycle for four SIMDs' 32 cycles per KB).
-constexpr int kWideStep = 64, kWideExtra = 2;
+constexpr int wide_extra(int dim) { return dim == 256 ? 6 : 8; }
+constexpr int wide_step(int dim) { return dim == 256 ? 64 : 32; }     // keys
+constexpr int wide_buffers(int dim) { return dim == 256 ? 2 : 4; }
 constexpr int wide_waves(int dim) { return dim == 256 ? 8 : 4; }
 constexpr int wide_tiles(bool exact) { return exact ? 1 : 2; }
 constexpr int wide_rows(int dim, bool exact) { return wide_waves(dim) * wide_tiles(exact) * 16; }
@@ -1019,10 +1074,11 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
 {
     constexpr bool kExact = std::is_same<Q, float>::value;
     constexpr int kWaves = wide_waves(D), kTiles = wide_tiles(kExact), kRows = wide_rows(D, kExact);
-    using R = Rows<D, T, kExact, kTiles>;
-    constexpr int kGroup = Lay<D>::kGroup, kGroups = kWideStep / 16, kBuf = kGroups * kGroup;
-    __shared__ __align__(128) uint8_t kbuf[2 * kBuf];
-    __shared__ __align__(128) uint8_t vbuf[2 * kBuf];
+    constexpr int kStep = wide_step(D), kBufs = wide_buffers(D), kExtra = wide_extra(D);
+    using R = Rows<D, T, kExact, kTiles, D < 256>;
+    constexpr int kGroup = Lay<D>::kGroup, kGroups = kStep / 16, kBuf = kGroups * kGroup;
+    __shared__ __align__(128) uint8_t kbuf[kBufs * kBuf];
+    __shared__ __align__(128) uint8_t vbuf[kBufs * kBuf];
     __shared__ int chunk_s[kWaves * 64];
     __shared__ int wave_s[kWaves], found_s[6];
     __shared__ unsigned long long strange_s;
@@ -1032,7 +1088,7 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
         strange_s = 0;
     Start st;
     unsigned per;
-    find_start<kRows, kWideStep, kWideExtra, kWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
+    find_start<kRows, kStep, kExtra, kWaves>(a, slots, slot, chunk_s, wave_s, found_s, st, per);
     unsigned line = (unsigned)slot * per;
     const unsigned end = min(line + per, (unsigned)st.all * (unsigned)a.kv_heads);
     Meta *meta = reinterpret_cast<Meta *>(a.meta) + slot;
@@ -1046,10 +1102,10 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
         R rows;
         rows.init_reads(lane);
         for (;;) {
-            span<kRows, kWideStep, kWideExtra>(a, u);
+            span<kRows, kStep, kExtra>(a, u);
             // [into, into + here) of the unit's place on the line: steps from .. to, if any
             const int here = (int)min((unsigned)(u.cost - into), end - line);
-            const int from = max(into - kWideExtra, 0), take = into + here - kWideExtra - from;
+            const int from = max(into - kExtra, 0), take = into + here - kExtra - from;
             if (take > 0) {
             const int unit0 = u.tile * kRows, nrows = min(u.n * a.group - unit0, kRows);
             const int row0 = unit0 + wave * kTiles * 16;
@@ -1082,51 +1138,69 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
             static_assert(kItems * kWaves == 2 * kGroups && kItems <= 2, "one item for each wave, or the keys and the values of a group");
             const int mine16 = (wave * kItems >> 1) * 16;
             auto load = [&](int step, int b, int id) {
-                const size_t at = at_of(id, step * kWideStep + mine16);
+                const size_t at = at_of(id, step * kStep + mine16);
                 const int to = b * kBuf + (wave * kItems >> 1) * kGroup;
                 if (kItems == 2 || !(wave & 1))
                     loader.load(a.k + at, (lds_t *)kbuf + to);
                 if (kItems == 2 || (wave & 1))
                     loader.load(a.v + at, (lds_t *)vbuf + to);
             };
-            // keys of a step that some row sees
-            constexpr uint64_t kAll = ~0ull;
-            static_assert(kWideStep == 64, "a bit for each key");
-            auto there_of = [&](int step) {
-                uint64_t there = key_bits(u.kbeg, u.kend, step * kWideStep) & kAll;
+            // The pages of a step's groups, read a step ahead; from them, the keys that some row sees
+            constexpr uint64_t kAll = kStep == 64 ? ~0ull : (1ull << kStep % 64) - 1;
+            int ids[kGroups];
+            auto read_ids = [&](int step) {
 #pragma unroll
                 for (int x = 0; x < kGroups; ++x)
-                    there &= (unsigned)id_of(step * kWideStep + 16 * x) < (unsigned)a.pages ? ~0ull : ~(0xffffull << (16 * x));
+                    ids[x] = id_of(step * kStep + 16 * x);
+            };
+            auto there_of = [&](int step) {
+                uint64_t there = kAll;
+                if (step * kStep < u.kbeg || (step + 1) * kStep > u.kend)
+                    there &= key_bits(u.kbeg, u.kend, step * kStep);
+#pragma unroll
+                for (int x = 0; x < kGroups; ++x)
+                    if ((unsigned)ids[x] >= (unsigned)a.pages)
+                        there &= ~(0xffffull << (16 * x));
                 return there;
             };
-            int next_id = id_of(first * kWideStep + mine16);
+            // the first steps' loads; the wave's page of the step after them; the first step's keys
+            int next_id = id_of(first * kStep + mine16);
             typename R::Raw raw;
             rows.fetch(a, u, head, row0, opaque(lane), raw);
-            load(first, 0, next_id);
-            next_id = id_of((first + 1) * kWideStep + mine16);
-            uint64_t next_there = there_of(first);
+#pragma unroll
+            for (int x = 0; x < kBufs - 1; ++x) {
+                if (x < take)
+                    load(first + x, x, next_id);
+                next_id = id_of((first + x + 1) * kStep + mine16);
+            }
+            read_ids(first);
             rows.begin(a, raw);
-            landed<0>();
-            __syncthreads();
             for (int x = 0; x < take; ++x) {
-                const int b = x & 1, step = first + x, step0 = step * kWideStep;
-                const uint64_t there = next_there;
+                const int b = x % kBufs, step = first + x, step0 = step * kStep;
+                // this step's loads have landed: of the wave's own by the wait, of the others' by the barrier; and what
+                // was read in the step before may be overwritten
+                if (take - 1 - x >= kBufs - 2)
+                    landed<kItems * Loader<D>::kLoads * (kBufs - 2)>();
+                else
+                    landed<0>();
+                __syncthreads();
+                const uint64_t there = there_of(step);
+                read_ids(step + 1);
                 uint64_t strange = 0;
-                if (step0 < unit_lo || step0 + kWideStep > unit_hi || there != kAll) {
-                    const uint64_t odd = any_of(clean<D, T, kWaves * 64, kWideStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
+                if (step0 < unit_lo || step0 + kStep > unit_hi || there != kAll) {
+                    const uint64_t odd = any_of(clean<D, T, kWaves * 64, kStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
                     if (odd && lane == 0)
                         atomicOr(&strange_s, (unsigned long long)odd);
                     __syncthreads();
                     strange = any_of(strange_s);
                 }
-                if (x + 1 < take) {
+                if (x + kBufs - 1 < take) {
                     loader.pin();
-                    load(step + 1, b ^ 1, next_id);
-                    next_id = id_of((step + 2) * kWideStep + mine16);
-                    next_there = there_of(step + 1);
+                    load(step + kBufs - 1, (x + kBufs - 1) % kBufs, next_id);
+                    next_id = id_of((step + kBufs) * kStep + mine16);
                 }
 #pragma unroll 1
-                for (int y = 0; y < kWideStep / kBlk; ++y) {
+                for (int y = 0; y < kStep / kBlk; ++y) {
                     const int key0 = step0 + y * kBlk;
                     if (key0 >= any_hi || key0 + kBlk <= any_lo)
                         continue;
@@ -1136,22 +1210,23 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
                     rows.scores(kb, s);
                     if (key0 < some_lo || key0 + kBlk > some_hi || ~mine)
                         rows.hide(a, key0, opaque(lane), mine, s);
+                    typename R::Values values;
+                    rows.read_ahead(vb, values);
                     uint4 p[kTiles][R::kParts];
                     rows.weigh(a, s, p);
                     for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
                         const int key = key0 + __builtin_ctz(odd);
                         rows.poison(a, key, a.v + at_of(id_of(key), key), opaque(lane));
                     }
-                    rows.add(vb, p);
+                    rows.add(vb, values, p);
                 }
-                landed<0>();
-                __syncthreads();
                 if (strange) {
+                    __syncthreads();   // all have read it
                     if (tid == 0)
                         strange_s = 0;
-                    __syncthreads();
                 }
             }
+            __syncthreads();
             rows.end();
             const bool begins = from == 0, ends = from + take == u.steps;
             // Through LDS, a column tile at a time, so that whole rows are written. (Both buffers have been read; a wave
@@ -1222,28 +1297,27 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
 // ---- units that a border cut ---------------------------------------------------------
 // o = sum_j 2^(c (m_j - m)) o_j and l likewise, over the parts in order, for the units that begin in a slot and end in
 // another.
-// Few rows, many parts: workgroup (slot, row). Its threads are as many groups as hold a row at a time, and
+// Few rows, many parts: workgroup (slot, y) takes every so many rows from row y on. Its threads are as many groups as hold a row at a time, and
 // a group takes every so many parts; their sums are added in the order of the groups.
-constexpr int kJoinThreads = 1024;
-
-template <int D, class Q>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_narrow_kernel(AttnArgs a)
+template <int D, class Q, int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_join_narrow_kernel(AttnArgs a)
 {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kWaves = kJoinThreads / 64, kMost = 768;
+    constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kWaves = THREADS / 64, kMost = 768;
     static_assert(narrow_per_cu(D) * 256 <= kMost, "as many parts as slots at most");
     __shared__ float weight_s[kMost];
-    __shared__ v4f sum_s[kJoinThreads];
+    __shared__ v4f sum_s[THREADS];
     __shared__ float wave_s[2][kWaves];
-    const int slot = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, group = tid / kLanes, d = tid % kLanes * 4;
+    const int slot = blockIdx.x, tid = threadIdx.x, group = tid / kLanes, d = tid % kLanes * 4;
     const Meta meta = reinterpret_cast<const Meta *>(a.meta)[slot];
-    if (meta.parts == 0 || meta.row0 + r >= meta.rows)
+    if (meta.parts == 0)
         return;
+    for (int r = blockIdx.y; r < kNarrowRows && meta.row0 + r < meta.rows; r += gridDim.y) {
     // part j, 0 of which is the slot's own
     auto part = [&](int j) { return part_of<kNarrowRows, D>(a, slot + j, j == 0); };
     constexpr int kM = kNarrowRows * D, kL = kM + kNarrowRows, kC = kL + kNarrowRows;
     const float c = part(0)[kC + r];
     float best = -INFINITY;
-    for (int j = tid; j < meta.parts; j += kJoinThreads) {
+    for (int j = tid; j < meta.parts; j += THREADS) {
         weight_s[j] = part(j)[kM + r];
         best = fmaxf(best, weight_s[j]);
     }
@@ -1257,7 +1331,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_narrow_kernel(AttnArgs
     for (int x = 0; x < kWaves; ++x)
         best = fmaxf(best, wave_s[0][x]);
     float l = 0.0f;
-    for (int j = tid; j < meta.parts; j += kJoinThreads) {
+    for (int j = tid; j < meta.parts; j += THREADS) {
         const float m = weight_s[j], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
         weight_s[j] = f;
         l += part(j)[kL + r] * f;
@@ -1295,6 +1369,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_narrow_kernel(AttnArgs
         for (int x = 1; x < kGroups; ++x)
             o += sum_s[x * kLanes + tid];
         put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+    }
+    __syncthreads();   // the next row's weights and sums take this one's place
     }
 }
 
@@ -1372,8 +1448,15 @@ int launch(const AttnArgs &a, hipStream_t st)
     constexpr int kRows = wide_rows(D, kExact);
     if (wide)
         hipLaunchKernelGGL((attn_join_wide_kernel<kRows, D, Q>), dim3(slots, kRows * D / 1024), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q>), dim3(slots, kNarrowRows), dim3(kJoinThreads), 0, st, a);
+    else {
+        // Rows of a request while decoding, and threads for the parts of a unit: with a few of them, 1024 threads a row
+        // cost more to start than they save (48 ragged requests: 9.9 us against 6; 1 of 131072: 8.1 against 15.6).
+        const dim3 grid(slots, a.tokens <= a.requests ? std::min(a.group, kNarrowRows) : kNarrowRows);
+        if ((long long)a.requests * a.kv_heads * 16 > slots)
+            hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q, 256>), grid, dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((attn_join_narrow_kernel<D, Q, 1024>), grid, dim3(1024), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? TB_OK : TB_EHIP;
 }
 
