@@ -592,7 +592,7 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  *             that share one must not overlap in time
  * scale > 0 and finite, heads a multiple of kv_heads, requests, tokens, width >= 1, window >= 0.
  * TB_EUNSUPPORTED unless dim is one of those above, requests <= 65536, tokens * heads < 2^30,
- * width * page <= 2^30 and (tokens * heads / 16 + requests * kv_heads) * (width * page / 64 + 4) < 2^31. */
+ * width * page <= 2^30 and (tokens * heads / 16 + requests * kv_heads) * (width * page / 32 + 10) < 2^31. */
 int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,
                   const int32_t *offsets, const int32_t *lengths, int requests, int tokens, float scale, int window,
                   void *out, void *ws, size_t ws_bytes, void *stream);

@@ -681,9 +681,10 @@ class Rope:
 
 def _heads(fn: str, name: str, t, device, rows: int, dim: int):
     """A view [rows][heads][dim] of wider rows as a tb_heads."""
-    if t.dim() != 3 or not t.is_cuda or t.device != device or t.shape[0] != rows or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[2] != dim or stride[2] != 1 or t.get_device() != device.index:
         _bad(fn, f"{name} has to be a tensor [{rows}][heads][{dim}] on {device} with consecutive elements of a head")
-    return CHeads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], _dtype(fn, t))
+    return CHeads(t.data_ptr(), stride[0], stride[1], shape[1], _dtype(fn, t))
 
 
 def tb_kv_plan(context, fresh, page: int, pages: int, table, free_list, count, lengths, offsets, positions, slots, left, missing,

@@ -127,6 +127,9 @@ __device__ __forceinline__ int opaque(int v)
     return v;
 }
 
+// What few blocks of keys meet: its code stands apart, and the others' together (2048 behind 8192: 313 -> 303 us)
+__device__ __forceinline__ bool rarely(bool v) { return __builtin_expect(v, 0); }
+
 __device__ __forceinline__ int by_group(const AttnArgs &a, int x)
 {
     return (int)((__umulhi((uint32_t)x, a.group_mul) + (uint32_t)x) >> a.group_shift);
@@ -605,7 +608,7 @@ struct Rows {
                            fmaxf(larger(s[n][1][0], s[n][1][1]), larger(s[n][1][2], s[n][1][3])));
             more |= (top[n] - m[n]) * c(a, n) > kLag;
         }
-        if (__any(more)) {
+        if (rarely(__any(more))) {
             bool fine = true;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -627,7 +630,7 @@ struct Rows {
             __builtin_amdgcn_sched_barrier(0);   // a tile's weights at a time
             const float base = m[n] == -INFINITY ? 0.0f : m[n];   // no key yet: all weights are 0
             float w[8];
-            if (!EXACT && small) {
+            if (!EXACT && !rarely(!small)) {
                 const float neg = __builtin_fmaf(-base, c(a, n), kBias);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -877,158 +880,159 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
             const int here = (int)min((unsigned)(u.cost - into), end - line);
             const int from = max(into - kNarrowExtra, 0), take = into + here - kNarrowExtra - from;
             if (take > 0) {
-            const int row0 = u.tile * kNarrowRows, nrows = min(u.n * a.group - row0, kNarrowRows);
+                const int row0 = u.tile * kNarrowRows, nrows = min(u.n * a.group - row0, kNarrowRows);
 
-            // all rows see keys from some_lo on up to some_hi; any row, those from kbeg on up to kend
-            int some_lo = 0, some_hi;
-            {
-                const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, row0 + nrows - 1);
-                some_hi = max(min(u.kend, p0 + 1), 0);
-                if (a.window)
-                    some_lo = max(p1 - a.window + 1, 0);
-            }
-            const int hi = min((u.s0 + from + take) * kNarrowStep, u.kend);
-            int blk = (u.s0 + from) * kNarrowWaves + wave;
-            while ((blk + 1) * kBlk <= u.kbeg)
-                blk += kNarrowWaves;
-            // The pages of a block's two groups of 16 keys, read a block ahead; then the groups' places. A group without a page
-            // is read from page 0, and not used.
-            auto ids_of = [&](int b, int (&id)[2]) {
+                // all rows see keys from some_lo on up to some_hi; any row, those from kbeg on up to kend
+                int some_lo = 0, some_hi;
+                {
+                    const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, row0 + nrows - 1);
+                    some_hi = max(min(u.kend, p0 + 1), 0);
+                    if (a.window)
+                        some_lo = max(p1 - a.window + 1, 0);
+                }
+                const int hi = min((u.s0 + from + take) * kNarrowStep, u.kend);
+                int blk = (u.s0 + from) * kNarrowWaves + wave;
+                while ((blk + 1) * kBlk <= u.kbeg)
+                    blk += kNarrowWaves;
+                // The pages of a block's two groups of 16 keys, read a block ahead; then the groups' places. A group without a page
+                // is read from page 0, and not used.
+                auto ids_of = [&](int b, int (&id)[2]) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    id[t] = table[(size_t)req * a.width + (min(b * kBlk + 16 * t, u.kend - 1) >> a.page_shift)];
-            };
-            auto place = [&](int b, const int (&id)[2], size_t (&at)[2]) {
+                    for (int t = 0; t < 2; ++t)
+                        id[t] = table[(size_t)req * a.width + (min(b * kBlk + 16 * t, u.kend - 1) >> a.page_shift)];
+                };
+                auto place = [&](int b, const int (&id)[2], size_t (&at)[2]) {
+                    uint32_t gone = 0;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int key = b * kBlk + 16 * t;
+                        const bool page = (unsigned)id[t] < (unsigned)a.pages;
+                        gone |= page && key < u.kend ? 0u : 1u << t;
+                        at[t] = ((((size_t)(page ? id[t] : 0) * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
+                    }
+                    return gone;
+                };
+                int id[2] = {-1, -1};
+                const bool any = blk * kBlk < hi;
+                if (any)
+                    ids_of(blk, id);
+                typename R::Raw raw;
+                rows.fetch(a, u, head, row0, opaque(lane), raw);
+                rows.begin(a, raw);
+                size_t at[2] = {0, 0};
                 uint32_t gone = 0;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int key = b * kBlk + 16 * t;
-                    const bool page = (unsigned)id[t] < (unsigned)a.pages;
-                    gone |= page && key < u.kend ? 0u : 1u << t;
-                    at[t] = ((((size_t)(page ? id[t] : 0) * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
-                }
-                return gone;
-            };
-            int id[2] = {-1, -1};
-            const bool any = blk * kBlk < hi;
-            if (any)
-                ids_of(blk, id);
-            typename R::Raw raw;
-            rows.fetch(a, u, head, row0, opaque(lane), raw);
-            rows.begin(a, raw);
-            size_t at[2] = {0, 0};
-            uint32_t gone = 0;
-            if (any) {
-                gone = place(blk, id, at);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    loader.load(a.k + at[t], kb + t * kGroup);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    loader.load(a.v + at[t], vb + t * kGroup);
-                ids_of(blk + kNarrowWaves, id);
-            }
-            while (blk * kBlk < hi) {
-                const int key0 = blk * kBlk, next = blk + kNarrowWaves;
-                const bool more = next * kBlk < hi;
-                size_t nat[2] = {0, 0};
-                uint32_t ngone = 0;
-                v4f s[1][2];
-                landed<2 * Loader<D>::kLoads>();   // all but the values, which were asked for last
-                rows.scores(kb, s);
-                lds_read();
-                if (more) {
-                    ngone = place(next, id, nat);
+                if (any) {
+                    gone = place(blk, id, at);
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        loader.load(a.k + nat[t], kb + t * kGroup);
+                        loader.load(a.k + at[t], kb + t * kGroup);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        loader.load(a.v + at[t], vb + t * kGroup);
+                    ids_of(blk + kNarrowWaves, id);
                 }
-                const bool whole = key0 >= some_lo && key0 + kBlk <= some_hi && !gone;
-                const uint32_t there = (uint32_t)key_bits(u.kbeg, u.kend, key0) & ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
-                if (!whole)
-                    rows.hide(a, key0, lane, there, s);
-                if (more)   // the next keys may be on their way
-                    landed<2 * Loader<D>::kLoads>();
-                else
-                    landed<0>();
-                uint64_t strange = 0;
-                if (!whole) {
-                    strange = any_of(clean<D, T, 64, kBlk>(vb, there, lane));
+                while (blk * kBlk < hi) {
+                    const int key0 = blk * kBlk, next = blk + kNarrowWaves;
+                    const bool more = next * kBlk < hi;
+                    size_t nat[2] = {0, 0};
+                    uint32_t ngone = 0;
+                    v4f s[1][2];
+                    landed<2 * Loader<D>::kLoads>();   // all but the values, which were asked for last
+                    rows.scores(kb, s);
                     lds_read();
-                }
-                typename R::Values values;
-                rows.read_ahead(vb, values);
-                uint4 p[1][R::kParts];
-                rows.weigh(a, s, p);
-                for (; strange; strange &= strange - 1) {
-                    const int x = __builtin_ctzll(strange), t = x >> 4;
-                    rows.poison(a, key0 + x, a.v + (t ? at[1] : at[0]) + (x & 15) * (D * 2), lane);
-                }
-                rows.add(vb, values, p);
-                lds_read();
-                if (more) {
+                    if (more) {
+                        ngone = place(next, id, nat);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        loader.load(a.v + nat[t], vb + t * kGroup);
-                    ids_of(next + kNarrowWaves, id);
+                        for (int t = 0; t < 2; ++t)
+                            loader.load(a.k + nat[t], kb + t * kGroup);
+                    }
+                    const bool whole = key0 >= some_lo && key0 + kBlk <= some_hi && !gone;
+                    const uint32_t there = (uint32_t)key_bits(u.kbeg, u.kend, key0) & ~((gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u));
+                    if (rarely(!whole))
+                        rows.hide(a, key0, lane, there, s);
+                    if (more)   // the next keys may be on their way
+                        landed<2 * Loader<D>::kLoads>();
+                    else
+                        landed<0>();
+                    uint64_t strange = 0;
+                    if (rarely(!whole)) {
+                        strange = any_of(clean<D, T, 64, kBlk>(vb, there, lane));
+                        lds_read();
+                    }
+                    typename R::Values values;
+                    rows.read_ahead(vb, values);
+                    uint4 p[1][R::kParts];
+                    rows.weigh(a, s, p);
+                    if (rarely(strange != 0))
+                        for (; strange; strange &= strange - 1) {
+                            const int x = __builtin_ctzll(strange), t = x >> 4;
+                            rows.poison(a, key0 + x, a.v + (t ? at[1] : at[0]) + (x & 15) * (D * 2), lane);
+                        }
+                    rows.add(vb, values, p);
+                    lds_read();
+                    if (more) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            loader.load(a.v + nat[t], vb + t * kGroup);
+                        ids_of(next + kNarrowWaves, id);
+                    }
+                    gone = ngone;
+                    at[0] = nat[0], at[1] = nat[1];
+                    blk = next;
                 }
-                gone = ngone;
-                at[0] = nat[0], at[1] = nat[1];
-                blk = next;
-            }
-            rows.end();
+                rows.end();
 
-            // the waves' sums become one, in the order of the waves
-            if (g == 0) {
-                m_s[wave][i] = rows.m[0];
-                l_s[wave][i] = rows.l[0];
-                c_s[i] = rows.c(a, 0);   // the same in all waves
-            }
-            __syncthreads();
-            float top = m_s[0][i];
-#pragma unroll
-            for (int w = 1; w < kNarrowWaves; ++w)
-                top = fmaxf(top, m_s[w][i]);
-            const float f = rows.m[0] == top ? 1.0f : __builtin_amdgcn_exp2f((rows.m[0] - top) * rows.c(a, 0));
-            float *mine = reinterpret_cast<float *>(kbuf + wave * kBuf);
-#pragma unroll
-            for (int d = 0; d < R::kO; ++d)
-                *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[0][d] * f;
-            __syncthreads();
-            const bool begins = from == 0, ends = from + take == u.steps;
-            for (int x = tid; x < kNarrowRows * D / 4; x += kNarrowWaves * 64) {
-                const int r = x / (D / 4), ch = x % (D / 4);
-                float best = m_s[0][r];
+                // the waves' sums become one, in the order of the waves
+                if (g == 0) {
+                    m_s[wave][i] = rows.m[0];
+                    l_s[wave][i] = rows.l[0];
+                    c_s[i] = rows.c(a, 0);   // the same in all waves
+                }
+                __syncthreads();
+                float top = m_s[0][i];
 #pragma unroll
                 for (int w = 1; w < kNarrowWaves; ++w)
-                    best = fmaxf(best, m_s[w][r]);
-                v4f o = {};
-                float l = 0.0f;
+                    top = fmaxf(top, m_s[w][i]);
+                const float f = rows.m[0] == top ? 1.0f : __builtin_amdgcn_exp2f((rows.m[0] - top) * rows.c(a, 0));
+                float *mine = reinterpret_cast<float *>(kbuf + wave * kBuf);
 #pragma unroll
-                for (int w = 0; w < kNarrowWaves; ++w) {
-                    o += *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(kbuf + w * kBuf) + r * D + (ch ^ r) * 4);
-                    const float mw = m_s[w][r];
-                    l += l_s[w][r] * (mw == best ? 1.0f : __builtin_amdgcn_exp2f((mw - best) * c_s[r]));
-                }
-                if (begins && ends) {
-                    if (r < nrows)
-                        put_out<Q, D>(a, u.first, row0 + r, head, ch * 4, o, l);
-                } else {
-                    float *part = part_of<kNarrowRows, D>(a, slot, begins);
-                    *reinterpret_cast<v4f *>(part + r * D + ch * 4) = o;
-                    if (ch == 0) {
-                        part[kNarrowRows * D + r] = best;
-                        part[kNarrowRows * D + kNarrowRows + r] = l;
-                        part[kNarrowRows * D + 2 * kNarrowRows + r] = c_s[r];
+                for (int d = 0; d < R::kO; ++d)
+                    *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[0][d] * f;
+                __syncthreads();
+                const bool begins = from == 0, ends = from + take == u.steps;
+                for (int x = tid; x < kNarrowRows * D / 4; x += kNarrowWaves * 64) {
+                    const int r = x / (D / 4), ch = x % (D / 4);
+                    float best = m_s[0][r];
+#pragma unroll
+                    for (int w = 1; w < kNarrowWaves; ++w)
+                        best = fmaxf(best, m_s[w][r]);
+                    v4f o = {};
+                    float l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kNarrowWaves; ++w) {
+                        o += *reinterpret_cast<const v4f *>(reinterpret_cast<const float *>(kbuf + w * kBuf) + r * D + (ch ^ r) * 4);
+                        const float mw = m_s[w][r];
+                        l += l_s[w][r] * (mw == best ? 1.0f : __builtin_amdgcn_exp2f((mw - best) * c_s[r]));
+                    }
+                    if (begins && ends) {
+                        if (r < nrows)
+                            put_out<Q, D>(a, u.first, row0 + r, head, ch * 4, o, l);
+                    } else {
+                        float *part = part_of<kNarrowRows, D>(a, slot, begins);
+                        *reinterpret_cast<v4f *>(part + r * D + ch * 4) = o;
+                        if (ch == 0) {
+                            part[kNarrowRows * D + r] = best;
+                            part[kNarrowRows * D + kNarrowRows + r] = l;
+                            part[kNarrowRows * D + 2 * kNarrowRows + r] = c_s[r];
+                        }
                     }
                 }
-            }
-            if (begins && !ends) {
-                // the unit's last place on the line is line - into + cost - 1
-                parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
-                if (tid == 0)
-                    *meta = Meta{parts, head, u.first, u.n * a.group, row0, {}};
-            }
+                if (begins && !ends) {
+                    // the unit's last place on the line is line - into + cost - 1
+                    parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
+                    if (tid == 0)
+                        *meta = Meta{parts, head, u.first, u.n * a.group, row0, {}};
+                }
             }
             line += here;
             if (line >= end)
@@ -1107,167 +1111,168 @@ __global__ __launch_bounds__(wide_waves(D) * 64, wide_waves(D) / 4 * wide_per_cu
             const int here = (int)min((unsigned)(u.cost - into), end - line);
             const int from = max(into - kExtra, 0), take = into + here - kExtra - from;
             if (take > 0) {
-            const int unit0 = u.tile * kRows, nrows = min(u.n * a.group - unit0, kRows);
-            const int row0 = unit0 + wave * kTiles * 16;
-            const bool active = row0 < unit0 + nrows;   // the wave has rows
-            // The wave's rows all see the keys from some_lo on up to some_hi; any of them, those from any_lo on up to any_hi.
-            int some_lo = 0, some_hi = 0, any_lo = 0, any_hi = 0;
-            if (active) {
-                const int last = min(row0 + kTiles * 16, unit0 + nrows) - 1;
-                const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, last);
-                some_hi = max(min(u.kend, p0 + 1), 0);
-                any_hi = max(min(u.kend, p1 + 1), 0);
-                if (a.window) {
-                    some_lo = max(p1 - a.window + 1, 0);
-                    any_lo = max(p0 - a.window + 1, 0);
-                }
-            }
-            const int first = u.s0 + from;
-            // all rows of the unit see the keys from unit_lo on up to unit_hi
-            const int unit_hi = min(u.kend, u.len - u.n + by_group(a, unit0) + 1);
-            const int unit_lo = a.window ? u.len - u.n + by_group(a, unit0 + nrows - 1) - a.window + 1 : 0;
-            // Of a step: group x of 16 keys; its page, if it has one; and the place of a key in the cache's arrays
-            auto id_of = [&](int key) { return table[(size_t)req * a.width + (min(key, max(u.kend - 1, 0)) >> a.page_shift)]; };
-            auto at_of = [&](int id, int key) {
-                id = (unsigned)id < (unsigned)a.pages ? id : 0;
-                return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
-            };
-            // The groups' keys and values are loaded by the waves in turn: items 2 x and 2 x + 1 are those of group x. A
-            // wave's pages are read a step ahead.
-            constexpr int kItems = 2 * kGroups / kWaves;
-            static_assert(kItems * kWaves == 2 * kGroups && kItems <= 2, "one item for each wave, or the keys and the values of a group");
-            const int mine16 = (wave * kItems >> 1) * 16;
-            auto load = [&](int step, int b, int id) {
-                const size_t at = at_of(id, step * kStep + mine16);
-                const int to = b * kBuf + (wave * kItems >> 1) * kGroup;
-                if (kItems == 2 || !(wave & 1))
-                    loader.load(a.k + at, (lds_t *)kbuf + to);
-                if (kItems == 2 || (wave & 1))
-                    loader.load(a.v + at, (lds_t *)vbuf + to);
-            };
-            // The pages of a step's groups, read a step ahead; from them, the keys that some row sees
-            constexpr uint64_t kAll = kStep == 64 ? ~0ull : (1ull << kStep % 64) - 1;
-            int ids[kGroups];
-            auto read_ids = [&](int step) {
-#pragma unroll
-                for (int x = 0; x < kGroups; ++x)
-                    ids[x] = id_of(step * kStep + 16 * x);
-            };
-            auto there_of = [&](int step) {
-                uint64_t there = kAll;
-                if (step * kStep < u.kbeg || (step + 1) * kStep > u.kend)
-                    there &= key_bits(u.kbeg, u.kend, step * kStep);
-#pragma unroll
-                for (int x = 0; x < kGroups; ++x)
-                    if ((unsigned)ids[x] >= (unsigned)a.pages)
-                        there &= ~(0xffffull << (16 * x));
-                return there;
-            };
-            // the first steps' loads; the wave's page of the step after them; the first step's keys
-            int next_id = id_of(first * kStep + mine16);
-            typename R::Raw raw;
-            rows.fetch(a, u, head, row0, opaque(lane), raw);
-#pragma unroll
-            for (int x = 0; x < kBufs - 1; ++x) {
-                if (x < take)
-                    load(first + x, x, next_id);
-                next_id = id_of((first + x + 1) * kStep + mine16);
-            }
-            read_ids(first);
-            rows.begin(a, raw);
-            for (int x = 0; x < take; ++x) {
-                const int b = x % kBufs, step = first + x, step0 = step * kStep;
-                // this step's loads have landed: of the wave's own by the wait, of the others' by the barrier; and what
-                // was read in the step before may be overwritten
-                if (take - 1 - x >= kBufs - 2)
-                    landed<kItems * Loader<D>::kLoads * (kBufs - 2)>();
-                else
-                    landed<0>();
-                __syncthreads();
-                const uint64_t there = there_of(step);
-                read_ids(step + 1);
-                uint64_t strange = 0;
-                if (step0 < unit_lo || step0 + kStep > unit_hi || there != kAll) {
-                    const uint64_t odd = any_of(clean<D, T, kWaves * 64, kStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
-                    if (odd && lane == 0)
-                        atomicOr(&strange_s, (unsigned long long)odd);
-                    __syncthreads();
-                    strange = any_of(strange_s);
-                }
-                if (x + kBufs - 1 < take) {
-                    loader.pin();
-                    load(step + kBufs - 1, (x + kBufs - 1) % kBufs, next_id);
-                    next_id = id_of((step + kBufs) * kStep + mine16);
-                }
-#pragma unroll 1
-                for (int y = 0; y < kStep / kBlk; ++y) {
-                    const int key0 = step0 + y * kBlk;
-                    if (key0 >= any_hi || key0 + kBlk <= any_lo)
-                        continue;
-                    const lds_t *kb = (const lds_t *)kbuf + b * kBuf + y * 2 * kGroup, *vb = (const lds_t *)vbuf + b * kBuf + y * 2 * kGroup;
-                    const uint32_t mine = (uint32_t)(there >> (32 * y));
-                    v4f s[kTiles][2];
-                    rows.scores(kb, s);
-                    if (key0 < some_lo || key0 + kBlk > some_hi || ~mine)
-                        rows.hide(a, key0, opaque(lane), mine, s);
-                    typename R::Values values;
-                    rows.read_ahead(vb, values);
-                    uint4 p[kTiles][R::kParts];
-                    rows.weigh(a, s, p);
-                    for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
-                        const int key = key0 + __builtin_ctz(odd);
-                        rows.poison(a, key, a.v + at_of(id_of(key), key), opaque(lane));
+                const int unit0 = u.tile * kRows, nrows = min(u.n * a.group - unit0, kRows);
+                const int row0 = unit0 + wave * kTiles * 16;
+                const bool active = row0 < unit0 + nrows;   // the wave has rows
+                // The wave's rows all see the keys from some_lo on up to some_hi; any of them, those from any_lo on up to any_hi.
+                int some_lo = 0, some_hi = 0, any_lo = 0, any_hi = 0;
+                if (active) {
+                    const int last = min(row0 + kTiles * 16, unit0 + nrows) - 1;
+                    const int p0 = u.len - u.n + by_group(a, row0), p1 = u.len - u.n + by_group(a, last);
+                    some_hi = max(min(u.kend, p0 + 1), 0);
+                    any_hi = max(min(u.kend, p1 + 1), 0);
+                    if (a.window) {
+                        some_lo = max(p1 - a.window + 1, 0);
+                        any_lo = max(p0 - a.window + 1, 0);
                     }
-                    rows.add(vb, values, p);
                 }
-                if (strange) {
-                    __syncthreads();   // all have read it
-                    if (tid == 0)
-                        strange_s = 0;
+                const int first = u.s0 + from;
+                // all rows of the unit see the keys from unit_lo on up to unit_hi
+                const int unit_hi = min(u.kend, u.len - u.n + by_group(a, unit0) + 1);
+                const int unit_lo = a.window ? u.len - u.n + by_group(a, unit0 + nrows - 1) - a.window + 1 : 0;
+                // Of a step: group x of 16 keys; its page, if it has one; and the place of a key in the cache's arrays
+                auto id_of = [&](int key) { return table[(size_t)req * a.width + (min(key, max(u.kend - 1, 0)) >> a.page_shift)]; };
+                auto at_of = [&](int id, int key) {
+                    id = (unsigned)id < (unsigned)a.pages ? id : 0;
+                    return ((((size_t)id * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * (D * 2);
+                };
+                // The groups' keys and values are loaded by the waves in turn: items 2 x and 2 x + 1 are those of group x. A
+                // wave's pages are read a step ahead.
+                constexpr int kItems = 2 * kGroups / kWaves;
+                static_assert(kItems * kWaves == 2 * kGroups && kItems <= 2, "one item for each wave, or the keys and the values of a group");
+                const int mine16 = (wave * kItems >> 1) * 16;
+                auto load = [&](int step, int b, int id) {
+                    const size_t at = at_of(id, step * kStep + mine16);
+                    const int to = b * kBuf + (wave * kItems >> 1) * kGroup;
+                    if (kItems == 2 || !(wave & 1))
+                        loader.load(a.k + at, (lds_t *)kbuf + to);
+                    if (kItems == 2 || (wave & 1))
+                        loader.load(a.v + at, (lds_t *)vbuf + to);
+                };
+                // The pages of a step's groups, read a step ahead; from them, the keys that some row sees
+                constexpr uint64_t kAll = kStep == 64 ? ~0ull : (1ull << kStep % 64) - 1;
+                int ids[kGroups];
+                auto read_ids = [&](int step) {
+#pragma unroll
+                    for (int x = 0; x < kGroups; ++x)
+                        ids[x] = id_of(step * kStep + 16 * x);
+                };
+                auto there_of = [&](int step) {
+                    uint64_t there = kAll;
+                    if (step * kStep < u.kbeg || (step + 1) * kStep > u.kend)
+                        there &= key_bits(u.kbeg, u.kend, step * kStep);
+#pragma unroll
+                    for (int x = 0; x < kGroups; ++x)
+                        if ((unsigned)ids[x] >= (unsigned)a.pages)
+                            there &= ~(0xffffull << (16 * x));
+                    return there;
+                };
+                // the first steps' loads; the wave's page of the step after them; the first step's keys
+                int next_id = id_of(first * kStep + mine16);
+                typename R::Raw raw;
+                rows.fetch(a, u, head, row0, opaque(lane), raw);
+#pragma unroll
+                for (int x = 0; x < kBufs - 1; ++x) {
+                    if (x < take)
+                        load(first + x, x, next_id);
+                    next_id = id_of((first + x + 1) * kStep + mine16);
                 }
-            }
-            __syncthreads();
-            rows.end();
-            const bool begins = from == 0, ends = from + take == u.steps;
-            // Through LDS, a column tile at a time, so that whole rows are written. (Both buffers have been read; a wave
-            // reads what its own lanes wrote.)
-            float *mine = reinterpret_cast<float *>(wave < kWaves / 2 ? kbuf : vbuf) + wave % (kWaves / 2) * (16 * D);
-            const int own = opaque(lane), i = own & 15, g = own >> 4;
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                const int r0 = wave * kTiles * 16 + 16 * n;   // of the unit
-#pragma unroll
-                for (int d = 0; d < R::kO; ++d)
-                    *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[n][d];
-                lds_read();
-                const float ln = rows.l[n], mn = rows.m[n], cn = rows.c(a, n);
+                read_ids(first);
+                rows.begin(a, raw);
+                for (int x = 0; x < take; ++x) {
+                    const int b = x % kBufs, step = first + x, step0 = step * kStep;
+                    // this step's loads have landed: of the wave's own by the wait, of the others' by the barrier; and what
+                    // was read in the step before may be overwritten
+                    if (take - 1 - x >= kBufs - 2)
+                        landed<kItems * Loader<D>::kLoads * (kBufs - 2)>();
+                    else
+                        landed<0>();
+                    __syncthreads();
+                    const uint64_t there = there_of(step);
+                    read_ids(step + 1);
+                    uint64_t strange = 0;
+                    if (rarely(step0 < unit_lo || step0 + kStep > unit_hi || there != kAll)) {
+                        const uint64_t odd = any_of(clean<D, T, kWaves * 64, kStep>((lds_t *)vbuf + b * kBuf, there, opaque(tid)));
+                        if (odd && lane == 0)
+                            atomicOr(&strange_s, (unsigned long long)odd);
+                        __syncthreads();
+                        strange = any_of(strange_s);
+                    }
+                    if (x + kBufs - 1 < take) {
+                        loader.pin();
+                        load(step + kBufs - 1, (x + kBufs - 1) % kBufs, next_id);
+                        next_id = id_of((step + kBufs) * kStep + mine16);
+                    }
 #pragma unroll 1
-                for (int x = own; x < 4 * D; x += 64) {
-                    const int r = x / (D / 4), ch = x % (D / 4);
-                    const v4f o = *reinterpret_cast<const v4f *>(mine + r * D + (ch ^ r) * 4);
-                    const float l = __shfl(ln, r), m = __shfl(mn, r), c = __shfl(cn, r);
-                    if (r0 + r >= nrows)
-                        continue;
-                    if (begins && ends) {
-                        put_out<Q, D>(a, u.first, unit0 + r0 + r, head, ch * 4, o, l);
-                    } else {
-                        float *part = part_of<kRows, D>(a, slot, begins);
-                        *reinterpret_cast<v4f *>(part + (r0 + r) * D + ch * 4) = o;
-                        if (ch == 0) {
-                            part[kRows * D + r0 + r] = m;
-                            part[kRows * D + kRows + r0 + r] = l;
-                            part[kRows * D + 2 * kRows + r0 + r] = c;
+                    for (int y = 0; y < kStep / kBlk; ++y) {
+                        const int key0 = step0 + y * kBlk;
+                        if (key0 >= any_hi || key0 + kBlk <= any_lo)
+                            continue;
+                        const lds_t *kb = (const lds_t *)kbuf + b * kBuf + y * 2 * kGroup, *vb = (const lds_t *)vbuf + b * kBuf + y * 2 * kGroup;
+                        const uint32_t mine = (uint32_t)(there >> (32 * y));
+                        v4f s[kTiles][2];
+                        rows.scores(kb, s);
+                        if (rarely(key0 < some_lo || key0 + kBlk > some_hi || ~mine))
+                            rows.hide(a, key0, opaque(lane), mine, s);
+                        typename R::Values values;
+                        rows.read_ahead(vb, values);
+                        uint4 p[kTiles][R::kParts];
+                        rows.weigh(a, s, p);
+                        if (rarely((uint32_t)(strange >> (32 * y)) != 0))
+                            for (uint32_t odd = (uint32_t)(strange >> (32 * y)); odd; odd &= odd - 1) {
+                                const int key = key0 + __builtin_ctz(odd);
+                                rows.poison(a, key, a.v + at_of(id_of(key), key), opaque(lane));
+                            }
+                        rows.add(vb, values, p);
+                    }
+                    if (strange) {
+                        __syncthreads();   // all have read it
+                        if (tid == 0)
+                            strange_s = 0;
+                    }
+                }
+                __syncthreads();
+                rows.end();
+                const bool begins = from == 0, ends = from + take == u.steps;
+                // Through LDS, a column tile at a time, so that whole rows are written. (Both buffers have been read; a wave
+                // reads what its own lanes wrote.)
+                float *mine = reinterpret_cast<float *>(wave < kWaves / 2 ? kbuf : vbuf) + wave % (kWaves / 2) * (16 * D);
+                const int own = opaque(lane), i = own & 15, g = own >> 4;
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    const int r0 = wave * kTiles * 16 + 16 * n;   // of the unit
+#pragma unroll
+                    for (int d = 0; d < R::kO; ++d)
+                        *reinterpret_cast<v4f *>(mine + i * D + ((4 * d + g) ^ i) * 4) = rows.o[n][d];
+                    lds_read();
+                    const float ln = rows.l[n], mn = rows.m[n], cn = rows.c(a, n);
+#pragma unroll 1
+                    for (int x = own; x < 4 * D; x += 64) {
+                        const int r = x / (D / 4), ch = x % (D / 4);
+                        const v4f o = *reinterpret_cast<const v4f *>(mine + r * D + (ch ^ r) * 4);
+                        const float l = __shfl(ln, r), m = __shfl(mn, r), c = __shfl(cn, r);
+                        if (r0 + r >= nrows)
+                            continue;
+                        if (begins && ends) {
+                            put_out<Q, D>(a, u.first, unit0 + r0 + r, head, ch * 4, o, l);
+                        } else {
+                            float *part = part_of<kRows, D>(a, slot, begins);
+                            *reinterpret_cast<v4f *>(part + (r0 + r) * D + ch * 4) = o;
+                            if (ch == 0) {
+                                part[kRows * D + r0 + r] = m;
+                                part[kRows * D + kRows + r0 + r] = l;
+                                part[kRows * D + 2 * kRows + r0 + r] = c;
+                            }
                         }
                     }
+                    lds_read();
                 }
-                lds_read();
-            }
-            __syncthreads();
-            if (begins && !ends) {
-                parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
-                if (tid == 0)
-                    *meta = Meta{parts, head, u.first, u.n * a.group, unit0, {}};
-            }
+                __syncthreads();
+                if (begins && !ends) {
+                    parts = (int)((line - (unsigned)into + (unsigned)u.cost - 1u) / per) - slot + 1;
+                    if (tid == 0)
+                        *meta = Meta{parts, head, u.first, u.n * a.group, unit0, {}};
+                }
             }
             line += here;
             if (line >= end)
@@ -1312,65 +1317,65 @@ __global__ __launch_bounds__(THREADS) void attn_join_narrow_kernel(AttnArgs a)
     if (meta.parts == 0)
         return;
     for (int r = blockIdx.y; r < kNarrowRows && meta.row0 + r < meta.rows; r += gridDim.y) {
-    // part j, 0 of which is the slot's own
-    auto part = [&](int j) { return part_of<kNarrowRows, D>(a, slot + j, j == 0); };
-    constexpr int kM = kNarrowRows * D, kL = kM + kNarrowRows, kC = kL + kNarrowRows;
-    const float c = part(0)[kC + r];
-    float best = -INFINITY;
-    for (int j = tid; j < meta.parts; j += THREADS) {
-        weight_s[j] = part(j)[kM + r];
-        best = fmaxf(best, weight_s[j]);
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1)
-        best = fmaxf(best, __shfl_xor(best, x));
-    if ((tid & 63) == 0)
-        wave_s[0][tid >> 6] = best;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kWaves; ++x)
-        best = fmaxf(best, wave_s[0][x]);
-    float l = 0.0f;
-    for (int j = tid; j < meta.parts; j += THREADS) {
-        const float m = weight_s[j], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
-        weight_s[j] = f;
-        l += part(j)[kL + r] * f;
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1)
-        l += __shfl_xor(l, x);
-    if ((tid & 63) == 0)
-        wave_s[1][tid >> 6] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kWaves; ++x)
-        l += wave_s[1][x];
-    v4f o = {};
-    constexpr int kAhead = 8;   // parts of a group whose loads are in flight
-    for (int j0 = group; j0 < meta.parts; j0 += kAhead * kGroups) {
-        v4f x[kAhead];
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            const int j = min(j0 + y * kGroups, meta.parts - 1);
-            x[y] = *reinterpret_cast<const v4f *>(part(j) + r * D + d);
+        // part j, 0 of which is the slot's own
+        auto part = [&](int j) { return part_of<kNarrowRows, D>(a, slot + j, j == 0); };
+        constexpr int kM = kNarrowRows * D, kL = kM + kNarrowRows, kC = kL + kNarrowRows;
+        const float c = part(0)[kC + r];
+        float best = -INFINITY;
+        for (int j = tid; j < meta.parts; j += THREADS) {
+            weight_s[j] = part(j)[kM + r];
+            best = fmaxf(best, weight_s[j]);
         }
 #pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            const int j = j0 + y * kGroups;
-            if (j < meta.parts)
-                o += x[y] * weight_s[j];
-        }
-    }
-    sum_s[tid] = o;
-    __syncthreads();
-    if (group == 0) {
+        for (int x = 1; x < 64; x <<= 1)
+            best = fmaxf(best, __shfl_xor(best, x));
+        if ((tid & 63) == 0)
+            wave_s[0][tid >> 6] = best;
+        __syncthreads();
 #pragma unroll
-        for (int x = 1; x < kGroups; ++x)
-            o += sum_s[x * kLanes + tid];
-        put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
-    }
-    __syncthreads();   // the next row's weights and sums take this one's place
+        for (int x = 0; x < kWaves; ++x)
+            best = fmaxf(best, wave_s[0][x]);
+        float l = 0.0f;
+        for (int j = tid; j < meta.parts; j += THREADS) {
+            const float m = weight_s[j], f = m == best ? 1.0f : __builtin_amdgcn_exp2f((m - best) * c);
+            weight_s[j] = f;
+            l += part(j)[kL + r] * f;
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1)
+            l += __shfl_xor(l, x);
+        if ((tid & 63) == 0)
+            wave_s[1][tid >> 6] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x)
+            l += wave_s[1][x];
+        v4f o = {};
+        constexpr int kAhead = 8;   // parts of a group whose loads are in flight
+        for (int j0 = group; j0 < meta.parts; j0 += kAhead * kGroups) {
+            v4f x[kAhead];
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y) {
+                const int j = min(j0 + y * kGroups, meta.parts - 1);
+                x[y] = *reinterpret_cast<const v4f *>(part(j) + r * D + d);
+            }
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y) {
+                const int j = j0 + y * kGroups;
+                if (j < meta.parts)
+                    o += x[y] * weight_s[j];
+            }
+        }
+        sum_s[tid] = o;
+        __syncthreads();
+        if (group == 0) {
+#pragma unroll
+            for (int x = 1; x < kGroups; ++x)
+                o += sum_s[x * kLanes + tid];
+            put_out<Q, D>(a, meta.first, meta.row0 + r, meta.head, d, o, l);
+        }
+        __syncthreads();   // the next row's weights and sums take this one's place
     }
 }
 
@@ -1512,9 +1517,9 @@ extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_k
     if (int rc = tbh::check_args(a, n))
         return rc;
     const long long limit = (long long)width * cache->page;
-    // steps of all units are counted in 31 bits
+    // the line of units, in steps of 32 keys at least and with what a unit costs beside them, is counted in 31 bits
     if (!can || limit > (1 << 30) ||
-        ((long long)tokens * q->heads / 16 + (long long)requests * cache->kv_heads) * (limit / 64 + 4) >= (1ll << 31))
+        ((long long)tokens * q->heads / 16 + (long long)requests * cache->kv_heads) * (limit / 32 + 10) >= (1ll << 31))
         return TB_EUNSUPPORTED;
     if (ws_bytes < need)
         return TB_EINVAL;

@@ -314,3 +314,122 @@ def test_refusals():
         tb.tb_attn_paged(**{**good, "cache": tb.KvCache(odd, odd.clone()), "q": q, "out": q.clone()})
     assert e.value.status == tb.TB_EUNSUPPORTED
     assert torch.all(c.out == 77.0)
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_chunks(dim, rows, cache):
+    """Chunks of many tiles beside single tokens, a window, pages that are none, values that are not finite: the kernel for many rows
+    at every width, its units cut by the borders of the workgroups' stretches."""
+    say(f"chunks dim={dim} {rows}/{cache}")
+    heads, kv = (6, 2) if dim < 256 else (5, 1)
+    for window in (0, 77):
+        c = Case([(331, 200), (9, 1), (64, 64), (700, 33), (1, 1)], heads, kv, dim, 32, rows, cache, seed=dim + window)
+        c.window = window
+        c.table[3, 4] = -1
+        c.set(0, 250, v=float("nan"))
+        c.set(0, 300, k=float("nan"))
+        c.v[c.table[2, 1], 0, 3, 5] = float("inf")
+        c.upload(extra=3).run().check()
+        assert torch.all(c.out[c.tokens:] == 77.0)
+
+
+@pytest.mark.parametrize("group", [1, 2, 5, 16, 17, 40])
+def test_groups(group):
+    """Heads of a kv head beside the tiles of 16 rows: fewer, as many, more, and more than one tile for a single token."""
+    say(f"group {group}")
+    Case([(300, 1), (45, 1), (0, 0)], group, 1, 64, 16, "bf16", "bf16", seed=group).upload().run().check()
+    Case([(300, 9), (45, 45)], group * 2, 2, 64, 16, "f32", "f16", seed=group).upload().run().check()
+
+
+def test_shared_pages_and_caches():
+    """Requests that share pages, a cache whose keys are its values, and a query row that all rows share."""
+    c = Case([(100, 1), (100, 1)], 4, 2, 64, 16, "bf16", "bf16", seed=21)
+    c.table[1, :5] = c.table[0, :5]
+    c.v = c.k.clone()
+    c.q[1] = c.q[0]
+    c.upload()
+    c.handle = tb.KvCache(c.dk, c.dk)
+    c.dq = c.dq[:1].expand(2, 4, 64)
+    c.run().check()
+
+
+def test_a_workspace_that_two_graphs_share():
+    """Two captured calls of different shapes, one workspace, replayed in turn."""
+    a = Case([(900, 1), (40, 1)], 16, 2, 256, 16, "bf16", "bf16", seed=22).upload()
+    b = Case([(700, 90), (50, 3)], 6, 2, 128, 16, "f16", "f16", seed=23).upload()
+    a.ws = b.ws = torch.full((max(a.ws.numel(), b.ws.numel()),), 0xFF, dtype=torch.uint8, device=gu.DEV)
+    wants = a.want(), b.want()
+    graphs = []
+    for c in (a, b):
+        c.run()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run()
+    for turn in range(4):
+        for c, g, w in zip((a, b), graphs, wants):
+            c.out.zero_()
+            g.replay()
+            c.check(w)
+            torch.randn(100, device=gu.DEV).sum().item()
+
+
+def test_a_layer_as_it_is_used():
+    """Prompt, then decoding, of two requests: plan -> fused projection -> rotation into the pages -> attention -> output
+    projection, with the ternary products, against the same steps in 64 bits on the projections' own rows."""
+    from ternary_weight_int8_tb_amd import synth
+    heads, kv, dim, page, hidden = 4, 1, 64, 16, 256
+    width = 2 * heads * dim + 2 * kv * dim
+    wq = tb.Matrix.upload(synth.matrix(synth.FMT_TERNARY2, width, hidden, 5, 0, synth.T_GATE))
+    wo = tb.Matrix.upload(synth.matrix(synth.FMT_TERNARY2, hidden, heads * dim, 5, 1, synth.T_DOWN))
+    pages, columns = 12, 6
+    cache = tb.KvCache(*(torch.full((pages, kv, page, dim), float("nan"), dtype=torch.bfloat16, device=gu.DEV) for _ in range(2)))
+    rope = tb.Rope.make(32, base=10000.0)
+    table = torch.full((2, columns), -1, dtype=torch.int32, device=gu.DEV)
+    free, count = ints(np.arange(pages)[::-1].copy()), ints([pages])
+    lengths, offsets = ints([0, 0]), ints([0, 0, 0])
+    missing = ints([0])
+    g = torch.Generator().manual_seed(1)
+    scale = float(np.float32(dim ** -0.5))
+    for fresh in ([19, 7], [1, 1], [1, 0], [1, 1], [0, 6]):
+        t = sum(fresh)
+        x = torch.randn(t, hidden, generator=g).to(gu.DEV)
+        positions, slots = gu.i32_out(t), gu.i32_out(t)
+        tb.tb_kv_plan(lengths, ints(fresh), page, pages, table, free, count, lengths, offsets, positions, slots, count, missing)
+        fused = gu.f32_out(t, width)
+        qx, dqx = gu.i8_out(t, hidden), gu.f32_out(t, hidden // 128)
+        for r in range(0, t, 8):      # eight rows a call
+            m = min(8, t - r)
+            tb.tb_gemv_ternary_x(wq, x[r:r + m], qx[r:r + m], dqx[r:r + m].contiguous(), fused[r:r + m])
+        fused *= 4.0
+        view = (lambda at, n: fused[:, at:at + n * dim].view(t, n, dim))
+        q, gate, k, v = view(0, heads), view(heads * dim, heads), view(2 * heads * dim, kv), view(2 * heads * dim + kv * dim, kv)
+        q_out, out = gu.f32_out(t, heads, dim), gu.f32_out(t, heads, dim)
+        tb.tb_rope_kv(q, k, v, rope, positions, slots, cache, q_out)
+        ws = torch.empty(tb.tb_attn_paged_workspace_bytes(cache, heads, torch.float32, 2, t), dtype=torch.uint8, device=gu.DEV)
+        tb.tb_attn_paged(q_out, cache, table, offsets, lengths, scale, out, ws, gate=gate)
+        y = gu.f32_out(t, hidden)
+        qh, dqh = gu.i8_out(t, heads * dim), gu.f32_out(t, heads * dim // 128)
+        for r in range(0, t, 8):
+            m = min(8, t - r)
+            tb.tb_gemv_ternary_x(wo, out.view(t, -1)[r:r + m], qh[r:r + m], dqh[r:r + m].contiguous(), y[r:r + m])
+        # the same steps in 64 bits
+        ln, off, tab = (gu.host(z) for z in (lengths, offsets, table))
+        assert int(gu.host(missing)[0]) == 0 and off[-1] == t and np.isfinite(gu.host(y)).all()
+        pos, slot = gu.host(positions), gu.host(slots)
+        for s in range(2):
+            n = off[s + 1] - off[s]
+            assert list(pos[off[s]:off[s + 1]]) == list(range(ln[s] - n, ln[s]))
+        freq = rope.freq.cpu().numpy()
+        for got, rows in ((q_out, q), (None, k)):
+            want, size = plain_kv.rope(rows.double().cpu().numpy(), pos, freq, 1.0, False)
+            if got is not None:
+                assert np.all(np.abs(gu.host(got) - want) <= size * 9 * plain_kv.U)
+            else:
+                kept = cache.k.float().cpu().numpy()[slot // page, :, slot % page]
+                assert np.all(np.abs(kept - want) <= size * 9 * plain_kv.U + 2.0 ** -8 * np.abs(want) * 1.001)
+        assert np.array_equal(cache.v.float().cpu().numpy()[slot // page, :, slot % page], v.to(torch.bfloat16).float().cpu().numpy())
+        want = plain_kv.attention(q_out.double().cpu().numpy(), cache.k.double().cpu().numpy(), cache.v.double().cpu().numpy(), tab, off, ln, scale,
+                                  0, gate.double().cpu().numpy())
+        assert np.all(np.abs(gu.host(out) - want[0]) <= plain_kv.attention_bound(*want, dim, "f32", "bf16"))
