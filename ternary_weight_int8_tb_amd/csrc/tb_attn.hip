@@ -837,8 +837,11 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int slot, bool begi
 // ---- few rows: a unit has 16 rows, its keys are split over the waves -----------------
 // A wave takes every fourth block of 32 keys, through buffers of its own: no barriers, and a wave's next keys are
 // on their way while it multiplies its values, and the other way round.
+// Bound: memory, behind a chain of latencies. One fp32 token of 16 heads over 131072 keys of 2 x 256 bf16: the loops
+// read 268 MB in 38 us, 7 TB/s; 9 us before them (the line of units 1.5, pages and q 2.8, the first keys) and 4 after; the
+// join 8. The same over 4096 keys: 15 us, of which no part is over 2, and 7.
 constexpr int kNarrowWaves = 4, kNarrowRows = 16, kNarrowStep = kNarrowWaves * kBlk;
-constexpr int kNarrowExtra = 2;
+constexpr int kNarrowExtra = 2;   // in steps: 48 ragged requests, 0: 71 us, 2: 47
 
 // workgroups of a CU: what LDS holds (128, 64 or 32 KB each), and registers
 constexpr int narrow_per_cu(int dim) { return dim == 256 ? 1 : dim == 128 ? 2 : 3; }
@@ -1062,9 +1065,16 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 }
 
 // ---- many rows: a unit has a tile of rows for each wave, which all read the same keys ----------------
-// 64 keys and their values at a time, in one of two buffers while the other is filled. With NT column tiles each
-// operand that is read from LDS enters NT instructions: at two, reading takes as long as multiplying (128
-// bytes a cycle for four SIMDs' 32 cycles per KB).
+// wide_step keys and their values at a time, in buffers of which one is multiplied while the others are filled. Each operand
+// that is read from LDS enters two instructions, for two tiles of 16 rows.
+//   D = 256: o and q take 192 of 256 registers, and the loop has none to spare. Eight waves share the buffers: with four of
+//   them in two workgroups a CU, the same number of cycles, but twice the loads, and a lower clock (357 us against 333).
+//   D = 128: two workgroups a CU, 32 keys a step and four buffers (a mixed step of 12 requests: 73 us; 64 keys and two
+//   buffers 75; eight waves that share 64 keys 77; three workgroups a CU the same as two).
+// Bound: the power limit and the loop's waits. 2048 new bf16 tokens behind 8192, 16 heads of 256: 303 us with the join, 1.02
+// PFLOP/s, at 1.8 to 2.0 GHz; the matrix cores are busy in 47% of the cycles, and vector operations take another 30%. A library
+// product of 8192^3 reaches 1.19 to 1.26.
+// wide_extra: what beginning and ending a unit takes, in steps (q and the first keys 6 us, rows out 4 to 11).
 constexpr int wide_extra(int dim) { return dim == 256 ? 6 : 8; }
 constexpr int wide_step(int dim) { return dim == 256 ? 64 : 32; }     // keys
 constexpr int wide_buffers(int dim) { return dim == 256 ? 2 : 4; }
@@ -1424,7 +1434,9 @@ __global__ __launch_bounds__(256) void attn_join_wide_kernel(AttnArgs a)
 }
 
 // ---- host ---------------------------------------------------------------------------
-// Which kernel: rows of 16 while the requests have few rows of a kv head each, on average.
+// Which kernel: units of 16 rows while the requests have no more of a kv head each, on average. Measured on both, at 2 x 256: 8
+// requests of 24 fp32 rows over 8192 keys 70 us with 16 rows a unit, 50 with many; 32 of 32 rows over 4096 78 and 77; 16 of 64
+// rows 63 and 57; at 8 x 128, 16 of 30 rows 80 and 73.
 bool is_wide(int group, int requests, int tokens) { return (long long)tokens * group > 16ll * requests; }
 
 // As many workgroups as the chip's 256 CUs hold at a time: a constant, as the order of the sums must not depend

@@ -17,6 +17,8 @@ using namespace tbr;
 // requests or a few entries a thread, and a second launch costs more than they do.
 // Pages taken and rows of the step are dealt to the threads, not requests: their numbers differ by
 // request from none to hundreds. A thread finds its request by a search in the scan, in LDS.
+// Bound: latency, of some twenty dependent accesses. 1 request 5 us; 250 requests, 2048 rows 11; 2048 requests, 16384
+// rows 28. (Four entries a thread with their loads in flight together: 8, 13 and 29.)
 // ------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxRequests = 16384;
@@ -221,7 +223,8 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a)
 // ------------------------------------------------------------------------------------
 // Rotary positions. A workgroup takes a token's heads of q, k and v: its angles are made once, into
 // LDS, and a thread turns 8 pairs at a time: 16 elements, which are two runs of 8 (half layout) or
-// one of 16 (interleaved, or not turned at all). Bound: memory.
+// one of 16 (interleaved, or not turned at all). Bound: memory (8192 bf16 tokens of 16 + 2 + 2 heads of 256: 168 MB in 36 us,
+// 4.6 TB/s; one token 3.9 us).
 // The angle, in turns, is reduced in fp64 to a quarter: positions of any size keep it to 2^-24.
 // ------------------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
