@@ -1071,9 +1071,9 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 //   them in two workgroups a CU, the same number of cycles, but twice the loads, and a lower clock (357 us against 333).
 //   D = 128: two workgroups a CU, 32 keys a step and four buffers (a mixed step of 12 requests: 73 us; 64 keys and two
 //   buffers 75; eight waves that share 64 keys 77; three workgroups a CU the same as two).
-// Bound: the power limit and the loop's waits. 2048 new bf16 tokens behind 8192, 16 heads of 256: 303 us with the join, 1.02
-// PFLOP/s, at 1.8 to 2.0 GHz; the matrix cores are busy in 47% of the cycles, and vector operations take another 30%. A library
-// product of 8192^3 reaches 1.19 to 1.26.
+// Bound: the power limit and the loop's waits. 2048 new bf16 tokens behind 8192, 16 heads of 256: 303 to 325 us with the join,
+// 0.95 to 1.02 PFLOP/s, at 1.8 to 2.0 GHz; the matrix cores are busy in 47% of the cycles, and vector operations take another
+// 30%. A library product of 8192^3 reaches 1.19 to 1.26.
 // wide_extra: what beginning and ending a unit takes, in steps (q and the first keys 6 us, rows out 4 to 11).
 constexpr int wide_extra(int dim) { return dim == 256 ? 6 : 8; }
 constexpr int wide_step(int dim) { return dim == 256 ? 64 : 32; }     // keys
