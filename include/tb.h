@@ -579,7 +579,9 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  * or NaN. A row whose scores are all -infinity has o = 0.
  * Products run on the matrix instructions of the cache's type. q of that type enters them as it is, and the
  * weights of the softmax are rounded to it; of fp32 rows q and the weights are split into parts whose sum has
- * 22 bits (fp16) or 24 (bf16).
+ * 22 bits (fp16) or 24 (bf16). With an fp16 cache the smallest have fewer: weights below 2^-15 of the row's largest are
+ * off by up to 2^-38 of that, elements of q below 2^-11 of the row's largest by up to 2^-34 of that; weights of fp16 rows
+ * below 2^-20 of the largest by up to 2^-31 of that.
  * The order of the sums, and so a row's low-order bits, depend on the lengths of all requests of the call;
  * the same call gives the same bits.
  *   q         [tokens][heads][dim], fp32 or the cache's type; dim 64, 128 or 256

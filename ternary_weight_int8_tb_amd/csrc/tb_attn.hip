@@ -76,7 +76,7 @@ __device__ __forceinline__ constexpr uint32_t exponents(Bf16) { return 0x7f807f8
 __device__ __forceinline__ constexpr uint32_t exponents(F16) { return 0x7c007c00u; }
 
 // fp32 values as parts in T whose sum has 24 bits (bf16: three parts, each cut off, not rounded, so that
-// the rest is exact) or 22 (fp16: two). One part: rounded to nearest.
+// the rest is exact) or 22 (fp16: two, as far as the second is above 2^-14: below it is off by 2^-25). One part: rounded to nearest.
 template <class T, bool EXACT>
 struct Split {
     static constexpr int kParts = 1;
@@ -411,8 +411,11 @@ __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)"
 template <int D, class T, bool EXACT, int NT, bool AHEAD>
 struct Rows {
     static constexpr int kQ = D / 32, kO = D / 16, kParts = Split<T, EXACT>::kParts;
-    // fp16 weights start at 2^6: small ones keep their bits, and a row whose maximum lags by kLag still fits
-    static constexpr float kBias = std::is_same<T, F16>::value ? 6.0f : 0.0f, kLag = 8.0f;
+    // fp16 weights start at 2^kBias: small ones keep their bits, and a row whose maximum lags by kLag still fits. Of fp32 rows
+    // a weight's second part must keep its bits too. Its last one is 2^-24: both parts are off by 2^-25 at most, 2^-38 of the largest
+    // weight, and the sum of 22 bits is whole from 2^-15 of that on. (At 2^6 weights of e^-16 would be off by up to 2^-8 of themselves.)
+    static constexpr bool kFine = EXACT && std::is_same<T, F16>::value;
+    static constexpr float kBias = kFine ? 13.0f : std::is_same<T, F16>::value ? 6.0f : 0.0f, kLag = kFine ? 2.0f : 8.0f;
     uint4 q[NT][kQ][kParts];
     v4f o[NT][kO];
     float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
@@ -423,8 +426,7 @@ struct Rows {
     uint32_t kread[kKk], vread[L::kKinds];   // the lane's places in a row of K, and of V
 
     // one factor for all rows, unless they have been scaled
-    static constexpr bool kScaled = EXACT && std::is_same<T, F16>::value;
-    __device__ __forceinline__ float c(const AttnArgs &a, int n) const { return kScaled ? factor[n] : a.scale; }
+    __device__ __forceinline__ float c(const AttnArgs &a, int n) const { return kFine ? factor[n] : a.scale; }
 
     __device__ __forceinline__ void init_reads(int lane)
     {
