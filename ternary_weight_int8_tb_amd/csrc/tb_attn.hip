@@ -420,7 +420,7 @@ struct Rows {
     v4f o[NT][kO];
     float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
     int pos[NT];                      // the row's position: it sees the keys up to it
-    bool small;                       // see weigh()
+    bool small;                       // all maxima are below kFused: see weigh()
     using L = Lay<D>;
     static constexpr int kKk = L::kApart ? 1 : L::kKinds / 2;
     uint32_t kread[kKk], vread[L::kKinds];   // the lane's places in a row of K, and of V
@@ -597,9 +597,13 @@ struct Rows {
     }
     // The weights of 32 keys, and what they do to the maximum and the sum. The maximum follows only when a score
     // exceeds it by kLag: until then weights are larger than one, which costs no bits, and o stays as it is.
-    // One fused operation scales a score and takes the maximum's product from it, which leaves that product's rounding in all
-    // of a row's exponents: less than 2^-4 while it is `small`, below 2^20, and gone with the sum. Larger ones, and fp32
-    // rows, for which all weights would have to be that much more exact, are subtracted first.
+    // One fused operation scales a score and takes the maximum's product from it. That product's rounding is in all exponents
+    // made under one maximum, but those of other waves, of other parts and of the keys before the maximum moved have another,
+    // and the joins know of neither: weights of two maxima are off against each other by up to 2^-23 of the product, times
+    // ln 2. Up to kFused that is 2^-10 (bf16) or 2^-13 (fp16), a quarter of the weights' own rounding. Under larger maxima, and for fp32
+    // rows, for which all weights would have to be that much more exact, scores are subtracted first. (With a limit of 2^20, sums
+    // of two maxima near scores of 7e5 were off by 4%.)
+    static constexpr float kFused = std::is_same<T, F16>::value ? 0x1p10f : 0x1p13f;
     __device__ __forceinline__ void weigh(const AttnArgs &a, const v4f (&s)[NT][2], uint4 (&p)[NT][kParts])
     {
         float top[NT];
@@ -619,7 +623,7 @@ struct Rows {
                 const float now = fmaxf(m[n], top[n]);
                 const float f = now > m[n] ? __builtin_amdgcn_exp2f((m[n] - now) * c(a, n)) : 1.0f;
                 m[n] = now;
-                fine &= fabsf(now) * c(a, n) < 0x1p20f || now == -INFINITY;
+                fine &= fabsf(now) * c(a, n) < kFused || now == -INFINITY;
                 l[n] *= f;
 #pragma unroll
                 for (int d = 0; d < kO; ++d)

@@ -61,3 +61,81 @@ def test_small_weights_of_fp32_rows(cache, new):
         bound = bound + want * 2.0 ** -38 / t
     off = np.abs(said(c) - want[..., None]) / bound[..., None]
     assert off.max() <= 1, off.max()
+
+
+# Below these products of a maximum and the scale's factor, a row's scores are scaled and the maximum's product taken from them in
+# one operation, so that all weights of one maximum have the rounding of that product: half a step of it
+FUSED = {"bf16": 2.0 ** 13, "f16": 2.0 ** 10}
+
+
+def base_error(score, kind):
+    """The relative error between weights of two maxima near `score`"""
+    at = score * np.log2(np.e)
+    return 2 * at * 2.0 ** -24 * np.log(2) * 1.01 if at < FUSED[kind] else 0.0
+
+
+SCORES = [700, 5600, 23170, 100003, 181071, 333337, 524287, 610101, 700001]
+
+
+def keys_of(score, dim):
+    """A key whose product with `query` is the whole number `score`, exactly, in either type: digits of at most 255"""
+    k = np.zeros(dim)
+    left, k[0] = score // 256, score % 256
+    for i in range(1, 16):
+        k[i] = min(left, 255)
+        left -= int(k[i])
+    assert left == 0
+    return k
+
+
+def query(dim):
+    q = np.zeros(dim)
+    q[0], q[1:16] = 1, 256
+    return q
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_large_scores_of_two_maxima(kind, dim):
+    """Scores that are whole numbers, and equal within each wave and each part: every weight is one, and what stands between
+    the sums is exp of the maxima's difference, whatever their magnitude."""
+    print(f"two maxima {kind} dim={dim}", flush=True)
+    n = 640
+    c = Case([(n, 1)] * len(SCORES), 2, 1, dim, 16, kind, kind, seed=2)
+    group = np.arange(n) // 32 % 2          # blocks of 32 keys go to the waves in turn
+    k = [np.where(group[:, None] == 1, keys_of(s + 1, dim), keys_of(s, dim)) for s in SCORES]
+    v = np.repeat((1.0 - 2 * group)[:, None], dim, 1)
+    fill(c, k, [v] * len(SCORES))
+    c.q[:] = torch.from_numpy(query(dim))
+    c.scale = 1.0
+    got = said(c.upload().run())
+    want = (1 - np.e) / (1 + np.e)
+    # exp of the difference 1: 3 U and the exponential's 4 U, in each of two joins; sums of ones are exact; the division and the type
+    bound = np.array([20 * U + base_error(s + 1, kind) for s in SCORES]) + HALF_STEP[kind] * abs(want)
+    off = np.abs(got - want).max((1, 2)) / bound
+    assert off.max() <= 1, off
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 40])
+def test_large_scores_whose_maximum_moves(kind, dim, new):
+    """Many equal scores, then a few that are 6 above them: the sums of the first are scaled by exp(-6)."""
+    print(f"maximum moves {kind} dim={dim} new={new}", flush=True)
+    n = 640
+    c = Case([(n, new)] * len(SCORES), 4, 1, dim, 16, kind, kind, seed=3)
+    top = (np.arange(n) >= 512) & (np.arange(n) % 32 == 0)
+    rest = (np.arange(n) >= 512) & ~top
+    k, v = [], np.repeat(np.where(top, -1.0, np.where(rest, 0.0, 1.0))[:, None], dim, 1)
+    for s in SCORES:
+        k.append(np.where(top[:, None], keys_of(s + 6, dim), np.where(rest[:, None], keys_of(s - 200, dim), keys_of(s, dim))))
+    fill(c, k, [v] * len(SCORES))
+    c.q[:] = torch.from_numpy(query(dim))
+    c.scale = 1.0
+    got = said(c.upload().run()).reshape(len(SCORES), new, -1)
+    # one of the four lies among the last tokens' own keys
+    high = np.array([top[:n - new + i + 1].sum() for i in range(new)]) * np.exp(6.0)
+    want = (512 - high) / (512 + high)
+    bound = (np.array([3 * 6 * U + 30 * U + base_error(s + 6, kind) for s in SCORES])[:, None] + HALF_STEP[kind] * np.abs(want))[..., None]
+    off = np.abs(got - want[:, None]) / bound
+    assert off.max() <= 1, off.max((1, 2))
