@@ -411,11 +411,16 @@ __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)"
 template <int D, class T, bool EXACT, int NT, bool AHEAD>
 struct Rows {
     static constexpr int kQ = D / 32, kO = D / 16, kParts = Split<T, EXACT>::kParts;
-    // fp16 weights start at 2^kBias: small ones keep their bits, and a row whose maximum lags by kLag still fits. Of fp32 rows
-    // a weight's second part must keep its bits too. Its last one is 2^-24: both parts are off by 2^-25 at most, 2^-38 of the largest
-    // weight, and the sum of 22 bits is whole from 2^-15 of that on. (At 2^6 weights of e^-16 would be off by up to 2^-8 of themselves.)
+    // Weights start at 2^kBias (of fp32 rows at kUnit, a factor: in the exponent it would cost bits), and a row's maximum lags by a
+    // factor of 2^kLag at most.
+    // bf16: so far below one that sums of the largest values that the cache holds are fp32 numbers. (2^30 keys of weights up to
+    // 2^-32; weights that fp32 has no more are 2^-86 of the largest.)
+    // fp16: so far above one that small weights keep their bits, and the largest, 2^14 or 2^15, still fits. Of fp32 rows a weight's
+    // second part must keep its bits too. Its last one is 2^-24: both parts are off by 2^-25 at most, 2^-38 of the largest weight, and
+    // the sum of 22 bits is whole from 2^-15 of that on. (At 2^6 weights of e^-16 would be off by up to 2^-8 of themselves.)
     static constexpr bool kFine = EXACT && std::is_same<T, F16>::value;
-    static constexpr float kBias = kFine ? 13.0f : std::is_same<T, F16>::value ? 6.0f : 0.0f, kLag = kFine ? 2.0f : 8.0f;
+    static constexpr float kBias = std::is_same<T, F16>::value ? 6.0f : -40.0f, kUnit = kFine ? 0x1p13f : 0x1p-40f;
+    static constexpr float kLag = kFine ? 2.0f : 8.0f;
     uint4 q[NT][kQ][kParts];
     v4f o[NT][kO];
     float m[NT], l[NT], factor[NT];   // running maximum of the scores, sum of the lane's weights, the scores' factor
@@ -644,11 +649,11 @@ struct Rows {
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    w[j] = __builtin_fmaf(s[n][j >> 2][j & 3] - base, c(a, n), kBias);
+                    w[j] = EXACT ? (s[n][j >> 2][j & 3] - base) * c(a, n) : __builtin_fmaf(s[n][j >> 2][j & 3] - base, c(a, n), kBias);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                w[j] = __builtin_amdgcn_exp2f(w[j]);
+                w[j] = __builtin_amdgcn_exp2f(w[j]) * (EXACT ? kUnit : 1.0f);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t parts[kParts];

@@ -139,3 +139,20 @@ def test_large_scores_whose_maximum_moves(kind, dim, new):
     bound = (np.array([3 * 6 * U + 30 * U + base_error(s + 6, kind) for s in SCORES])[:, None] + HALF_STEP[kind] * np.abs(want))[..., None]
     off = np.abs(got - want[:, None]) / bound
     assert off.max() <= 1, off.max((1, 2))
+
+
+@pytest.mark.parametrize("rows", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 3), (256, 1), (256, 60)])
+def test_large_values(rows, dim, new):
+    """Values near the largest that bf16 holds: their mean is finite, and so is what is returned."""
+    print(f"large values {rows} dim={dim} new={new}", flush=True)
+    n = 700
+    c = Case([(n, new)], 4, 2, dim, 16, rows, "bf16", seed=4)
+    fill(c, [np.zeros((n, dim))], [np.full((n, dim), 1.5 * 2.0 ** 127)])
+    got = said(c.upload().run())
+    assert np.all(np.abs(got / (1.5 * 2.0 ** 127) - 1) <= (2 * n + 20) * U)
+    # scores that grow, so that weights begin far above one
+    c.k[:] = (torch.randn(c.k.shape, generator=torch.Generator().manual_seed(5)) * 2).to(c.k.dtype)
+    c.upload().run()
+    got = said(c)
+    assert np.isfinite(got).all() and np.all(np.abs(got / (1.5 * 2.0 ** 127) - 1) <= (2 * n + 20) * U + (HALF_STEP["bf16"] if rows == "bf16" else 0))
