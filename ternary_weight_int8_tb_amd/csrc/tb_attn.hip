@@ -529,7 +529,9 @@ struct Rows {
                     v[x] = v[x] * f * f2;
                 e[s].set(v);
             }
-            factor[n] = a.scale / f / f2;
+            // Not 0 and not infinite, whose products with hidden scores and with the maximum's own difference are NaN. (Scores are
+            // below 2^35, and their differences above 2^-50: beyond these limits all weights are alike, or one is all.)
+            factor[n] = fminf(fmaxf(a.scale / f / f2, 0x1p-126f), 0x1.fffffep127f);
         }
 #pragma unroll
         for (int s = 0; s < kQ; ++s) {

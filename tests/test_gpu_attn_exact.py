@@ -156,3 +156,31 @@ def test_large_values(rows, dim, new):
     c.upload().run()
     got = said(c)
     assert np.isfinite(got).all() and np.all(np.abs(got / (1.5 * 2.0 ** 127) - 1) <= (2 * n + 20) * U + (HALF_STEP["bf16"] if rows == "bf16" else 0))
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+def test_tiny_and_large_scales(rows, cache):
+    """Scales at both ends, with keys that are hidden: all weights alike, or one."""
+    n, new, dim = 90, 20, 64
+    for scale, unit in ((1e-44, 1.0), (2.0 ** -126, 1.0), (2.0 ** 126, 1.0), (1e-5, 2.0 ** -126), (2.0 ** -60, 2.0 ** -140), (2.0 ** 20, 2.0 ** 118),
+                        (2.0 ** 120, 2.0 ** 60)):
+        if unit != 1.0 and rows != "f32":
+            continue
+        print(f"scale {scale:g} of rows of {unit:g} {rows}/{cache}", flush=True)
+        c = Case([(n, new)], 2, 1, dim, 16, rows, cache, seed=6)
+        best = 37
+        k = np.zeros((n, dim))
+        k[:, 0] = -1.0 - np.arange(n) % 7
+        k[best, 0] = 1.0
+        v = np.arange(n)[:, None] % 5 + np.zeros((n, dim))
+        fill(c, [k], [v])
+        c.q[:] = 0
+        c.q[..., 0] = unit
+        c.scale = float(np.float32(scale))
+        got = said(c.upload().run())
+        alike = c.scale * unit < 1
+        for i in range(new):
+            seen = n - new + i + 1
+            want = v[:seen, 0].mean() if alike else v[best, 0]
+            # whole numbers: their sums are exact
+            assert np.all(np.abs(got[i] - want) <= (HALF_STEP[rows] + 8 * U) * abs(want)), (scale, i, got[i, 0, 0], want)
