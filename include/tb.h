@@ -592,7 +592,7 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  *   out       q's type [tokens][heads][dim] output; rows of no request are left as they were
  *   ws        workspace of tb_attn_paged_workspace_bytes bytes, 16-byte aligned; no initialisation. Calls
  *             that share one must not overlap in time
- * scale > 0 and finite, heads a multiple of kv_heads, requests, tokens, width >= 1, window >= 0.
+ * scale > 0 and scale * log2(e) finite in fp32, heads a multiple of kv_heads, requests, tokens, width >= 1, window >= 0.
  * TB_EUNSUPPORTED unless dim is one of those above, requests <= 65536, tokens * heads < 2^30,
  * width * page <= 2^30 and (tokens * heads / 16 + requests * kv_heads) * (width * page / 32 + 10) < 2^31. */
 int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,

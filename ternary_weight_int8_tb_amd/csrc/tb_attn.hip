@@ -1518,7 +1518,7 @@ extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_k
                              const int32_t *offsets, const int32_t *lengths, int requests, int tokens, float scale, int window,
                              void *out, void *ws, size_t ws_bytes, void *stream)
 {
-    if (!q || !cache || !shapes_ok(*cache, q->heads, q->dtype, requests, tokens) || width < 1 || window < 0 || !(scale > 0.0f) || scale > 3.0e38f)
+    if (!q || !cache || !shapes_ok(*cache, q->heads, q->dtype, requests, tokens) || width < 1 || window < 0 || !(scale > 0.0f && scale * kLog2e < INFINITY))
         return TB_EINVAL;
     const int dim = cache->dim;
     if (gate && gate->heads != q->heads)
