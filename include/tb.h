@@ -587,7 +587,8 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  *   q         [tokens][heads][dim], fp32 or the cache's type; dim 64, 128 or 256
  *   gate      null, or rows like q's, of any type
  *   table     int32 [requests][width]
- *   offsets   int32 [requests + 1], from 0 on, not descending; lengths int32 [requests], up to 2^30
+ *   offsets   int32 [requests + 1], from 0 on, not descending (ones below 0 count as 0, ones above tokens as tokens; if
+ *             they descend, nothing is written to out); lengths int32 [requests], up to 2^30
  *   window    0: none
  *   out       q's type [tokens][heads][dim] output; rows of no request are left as they were
  *   ws        workspace of tb_attn_paged_workspace_bytes bytes, 16-byte aligned; no initialisation. Calls

@@ -150,6 +150,11 @@ __device__ __forceinline__ void request_of(const AttnArgs &a, int r, int &first,
     n = min(max(a.offsets[r + 1], first), a.tokens) - first;
     len = min(max(a.lengths[r], 0), 1 << 30);
 }
+// Offsets that descend give rows to several requests, and a line of units longer than the host has checked: such a call does nothing.
+__device__ __forceinline__ bool descends(const AttnArgs &a, int r)
+{
+    return min(max(a.offsets[r + 1], 0), a.tokens) < min(max(a.offsets[r], 0), a.tokens);
+}
 template <int ROWS>
 __device__ __forceinline__ int tiles_of(const AttnArgs &a, int n)
 {
@@ -236,6 +241,11 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
         W w;
         w.r = lane;
         int cost = 0;
+        if (__any(lane < a.requests && descends(a, lane))) {
+            st.all = 0;
+            per = 1;
+            return;
+        }
         if (lane < a.requests) {
             w.open(a);
             while (w.r == lane && w.left) {
@@ -275,13 +285,19 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int slots, int slo
     const int tid = threadIdx.x, chunk = (a.requests + kThreads - 1) / kThreads;
     const int q0 = min(tid * chunk, a.requests), q1 = min(q0 + chunk, a.requests);
     int tiles = 0, first, n, len, total;
+    bool none = false;
     for (int r = q0; r < q1; ++r) {
         request_of(a, r, first, n, len);
         tiles += tiles_of<ROWS>(a, n);
+        none |= descends(a, r);
     }
-    const int before = scan<WAVES>(tiles, wave_s, total);
+    const int before = scan<WAVES>(none ? 0 : tiles, wave_s, total);
     chunk_s[tid] = before;
-    __syncthreads();
+    if (__syncthreads_or(none)) {
+        st.all = 0;
+        per = 1;
+        return;
+    }
     const int share = (total + kThreads - 1) / kThreads, t0 = min(tid * share, total), t1 = min(t0 + share, total);
     // the chunk, then the request, of tile t0
     W w;

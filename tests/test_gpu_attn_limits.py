@@ -1,0 +1,100 @@
+"""Attention over a paged cache: arguments outside the contract that reach nothing beside the outputs, and paths that only
+sizes beyond the ordinary take."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import ternary_weight_int8_tb_amd as tb
+from tests import gpu_util as gu
+from tests.test_gpu_attn_paged import KINDS, TYPES, Case, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    yield
+
+
+class Guarded:
+    """A tensor within a larger one, with 64 KB of 0x3C on either side."""
+
+    EDGE = 65536
+
+    def __init__(self, like):
+        n = like.numel() * like.element_size()
+        self.all = torch.full((n + 2 * self.EDGE,), 0x3C, dtype=torch.uint8, device=gu.DEV)
+        self.t = self.all[self.EDGE:self.EDGE + n].view(like.dtype).view(like.shape)
+        self.t.copy_(like)
+
+    def whole(self):
+        return bool((self.all[:self.EDGE] == 0x3C).all() and (self.all[-self.EDGE:] == 0x3C).all())
+
+
+def guarded_run(c):
+    """Runs a case with out and ws guarded; nothing beside them has changed."""
+    out, ws = Guarded(c.out), Guarded(c.ws)
+    c.out, c.ws = out.t, ws.t
+    kept = {n: getattr(c, n).clone().view(torch.uint8) for n in ("dq", "dk", "dv", "dt", "do", "dl")}
+    c.run()
+    torch.cuda.synchronize()
+    assert out.whole() and ws.whole()
+    for n, was in kept.items():
+        assert torch.equal(getattr(c, n).view(torch.uint8), was), n
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+@pytest.mark.parametrize("offsets,lengths", [([0, 100, 2, 2 ** 31 - 1], [40, 50, 60]), ([-5, 3, -2, 9], [40, -50, 2 ** 31 - 1]),
+                                             ([12, 0, 12, 0], [1, 2, 3]), ([2 ** 31 - 1, -2 ** 31, 5, 6], [10 ** 9, 50, 60])])
+def test_offsets_that_descend(rows, cache, offsets, lengths):
+    """Nothing is written."""
+    c = Case([(40, 4), (50, 4), (60, 4)], 4, 2, 64, 16, rows, cache, seed=10).upload(extra=2)
+    c.do, c.dl = ints(offsets), ints(lengths)
+    guarded_run(c)
+    assert torch.all(c.out == 77.0)
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+def test_offsets_outside_the_rows(rows, cache):
+    """Offsets that do not descend count as the nearest row: requests before and behind the rows have none."""
+    c = Case([(40, 4), (50, 4), (60, 4)], 4, 2, 64, 16, rows, cache, seed=10).upload(extra=2)
+    c.do = ints([-7, 4, 8, 2 ** 31 - 1])       # as [0, 4, 8, 14]
+    guarded_run(c)
+    first, got = c.out[:8].clone(), c.out[8:].clone()
+    c.do = ints([0, 4, 8, 14])
+    c.dq = torch.where(torch.isnan(c.dq), torch.zeros_like(c.dq), c.dq)
+    c.out.fill_(77.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out[:8], first) and torch.equal(c.out[8:12], got[:4])
+    # one row for each request, as in decoding, and then rows of none
+    d = Case([(40, 1), (50, 1), (60, 1), (9, 1), (0, 0)], 4, 2, 64, 16, rows, cache, seed=11).upload(extra=1)
+    d.do = ints([-1, 1, 2, 3, 2 ** 31 - 1, 2 ** 31 - 1])
+    guarded_run(d)
+    first = d.out[:3].clone()
+    d.do = ints([0, 1, 2, 3, 3, 3])
+    d.out.fill_(77.0)
+    d.run()
+    torch.cuda.synchronize()
+    assert torch.equal(d.out[:3], first) and torch.all(d.out[3:] == 77.0)
+
+
+@pytest.mark.parametrize("requests,tokens", [(4096, 65536), (4096, 4096), (64, 64)])
+def test_requests_that_all_claim_all_rows(requests, tokens):
+    """Together more units than 31 bits count, if each were taken at its word."""
+    heads, kv, dim, width, page = 16, 2, 64, 1024, 16
+    q = torch.randn(tokens, heads, dim, device=gu.DEV).to(torch.bfloat16)
+    k = torch.randn(3, kv, page, dim, device=gu.DEV).to(torch.bfloat16)
+    cache = tb.KvCache(k, k.clone())
+    table = torch.zeros(requests, width, dtype=torch.int32, device=gu.DEV)
+    offsets = ints(np.where(np.arange(requests + 1) % 2 == 1, tokens, 0))
+    lengths = ints(np.full(requests, 2 ** 31 - 1))
+    out = Guarded(torch.full_like(q, 77.0))
+    ws = Guarded(torch.zeros(tb.tb_attn_paged_workspace_bytes(cache, heads, q.dtype, requests, tokens), dtype=torch.uint8, device=gu.DEV))
+    tb.tb_attn_paged(q, cache, table, offsets, lengths, 0.125, out.t, ws.t)
+    torch.cuda.synchronize()
+    assert out.whole() and ws.whole() and torch.all(out.t == 77.0)
