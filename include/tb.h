@@ -582,6 +582,8 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  * 22 bits (fp16) or 24 (bf16). With an fp16 cache the smallest have fewer: weights below 2^-15 of the row's largest are
  * off by up to 2^-38 of that, elements of q below 2^-11 of the row's largest by up to 2^-34 of that; weights of fp16 rows
  * below 2^-20 of the largest by up to 2^-31 of that.
+ * Where tokens > requests the call is made for chunks, else for single tokens of each request. A prompt among as many requests
+ * that wait takes longer than by itself: its time is best with the waiting ones left out of the call.
  * The order of the sums, and so a row's low-order bits, depend on the lengths of all requests of the call;
  * the same call gives the same bits.
  *   q         [tokens][heads][dim], fp32 or the cache's type; dim 64, 128 or 256

@@ -1463,10 +1463,20 @@ __global__ __launch_bounds__(256) void attn_join_wide_kernel(AttnArgs a)
 }
 
 // ---- host ---------------------------------------------------------------------------
-// Which kernel: units of 16 rows while the requests have no more of a kv head each, on average. Measured on both, at 2 x 256: 8
-// requests of 24 fp32 rows over 8192 keys 70 us with 16 rows a unit, 50 with many; 32 of 32 rows over 4096 78 and 77; 16 of 64
-// rows 63 and 57; at 8 x 128, 16 of 30 rows 80 and 73.
-bool is_wide(int group, int requests, int tokens) { return (long long)tokens * group > 16ll * requests; }
+// Which kernel. The host knows no request's rows, only their sum. Times below are us with the kernel for few rows / for many, bf16.
+//   More tokens than requests: one of them has several; it has (tokens - requests + 1) * group rows if the others bring one
+//   each, and from 128 on the kernel for many rows runs. Beside a chunk it takes 0 to 40% longer for decodes, but the other one
+//   walks all keys again for every 16 rows of the chunk. 16 heads on 2 x 256: 250 decodes of up to 8192 and 1000 tokens 527 / 337; 48
+//   and 500 172 / 107; 12 and 64 behind 1000 33 / 46; 1 x 8 tokens behind 8192 34 / 54; 8 x 4 66 / 48; 64 x 4 210 / 213; 64 x 16
+//   770 / 243. 24 heads on 8 x 128: 250 decodes and 1000 tokens 444 / 379; 64 x 4 behind 4096 192 / 205.
+//   Else, as in decoding, a request has a token's heads. With more than 16 on a kv head, and many requests, they share their keys:
+//   32 heads on 1 x 128 of 4 requests 30 / 66, of 32 42 / 31, of 128 55 / 45; 64 on 1 x 256 of 4 32 / 58, of 128 154 / 77.
+//   (Requests that wait count here: 2048 tokens of one among 2048 are taken for decodes, 844 / 524.)
+bool is_wide(int group, int requests, int tokens)
+{
+    const long long rows = (long long)tokens * group;
+    return tokens > requests ? rows - (long long)(requests - 1) * group > 128 : group > 16 && rows >= 1024;
+}
 
 // As many workgroups as the chip's 256 CUs hold at a time: a constant, as the order of the sums must not depend
 // on a partition's size.

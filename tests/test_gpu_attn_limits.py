@@ -98,3 +98,16 @@ def test_requests_that_all_claim_all_rows(requests, tokens):
     tb.tb_attn_paged(q, cache, table, offsets, lengths, 0.125, out.t, ws.t)
     torch.cuda.synchronize()
     assert out.whole() and ws.whole() and torch.all(out.t == 77.0)
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+@pytest.mark.parametrize("requests,group,dim,kv", [
+    ([(300, 1)] * 3, 40, 64, 1), ([(70, 1), (0, 0), (41, 1)] * 9, 64, 64, 1), ([(65, 1)] * 9, 128, 128, 1), ([(40, 1)] * 17, 33, 256, 2),   # decodes
+    ([(33, 1)] * 40 + [(150, 60)], 3, 128, 2), ([(90, 5)], 8, 256, 2), ([(64, 2)] * 12, 4, 64, 1), ([(20, 0)] * 50 + [(50, 50)], 8, 64, 1)])
+def test_either_kernel(rows, cache, requests, group, dim, kv):
+    """Decodes with more heads than a tile has rows, few and many; chunks beside decodes and beside requests that wait."""
+    print(f"either kernel {len(requests)} requests group={group} dim={dim} {rows}/{cache}", flush=True)
+    c = Case(requests, group * kv, kv, dim, 16, rows, cache, seed=group)
+    c.upload()
+    guarded_run(c)
+    c.check()
