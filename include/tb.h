@@ -601,7 +601,8 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
 int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,
                   const int32_t *offsets, const int32_t *lengths, int requests, int tokens, float scale, int window,
                   void *out, void *ws, size_t ws_bytes, void *stream);
-/* Workspace bytes for q rows of `dtype` (0 for arguments that the call refuses). */
+/* Workspace bytes for q rows of `dtype`, enough for every call with at most these requests and tokens (0 for arguments
+ * that the call refuses). */
 size_t tb_attn_paged_workspace_bytes(const tb_kv_cache *cache, int heads, int dtype, int requests, int tokens);
 
 /* Static description of a status code; never NULL. */

@@ -740,7 +740,7 @@ def tb_rope_kv(q, k, v, rope: Rope | None, positions, slots, cache: KvCache | No
 
 
 def tb_attn_paged_workspace_bytes(cache: KvCache, heads: int, dtype, requests: int, tokens: int) -> int:
-    """Bytes of device workspace tb_attn_paged needs for q rows of a torch dtype."""
+    """Bytes of device workspace tb_attn_paged needs for q rows of a torch dtype, with at most these requests and tokens."""
     torch = _torch()
     code = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.float16: TB_F16}.get(dtype, -1)
     return int(lib().tb_attn_paged_workspace_bytes(cache.ref, int(heads), code, int(requests), int(tokens)))

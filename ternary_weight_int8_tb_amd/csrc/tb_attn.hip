@@ -1533,11 +1533,16 @@ bool runs(const tb_kv_cache &c, int heads, int requests, int tokens)
 
 }  // namespace
 
+// Enough for every call with at most these requests and tokens, whichever kernel it takes (see is_wide; a call wants its own kernel's)
 extern "C" size_t tb_attn_paged_workspace_bytes(const tb_kv_cache *cache, int heads, int dtype, int requests, int tokens)
 {
     if (!cache || !shapes_ok(*cache, heads, dtype, requests, tokens) || !runs(*cache, heads, requests, tokens))
         return 0;
-    return workspace(is_wide(heads / cache->kv_heads, requests, tokens), cache->dim, dtype == TB_F32);
+    const int group = heads / cache->kv_heads;
+    // one request with all the tokens; or one token of each of as many requests
+    const bool wide = is_wide(group, 1, tokens) || is_wide(group, std::min(requests, tokens), std::min(requests, tokens));
+    const size_t few = workspace(false, cache->dim, dtype == TB_F32);
+    return wide ? std::max(few, workspace(true, cache->dim, dtype == TB_F32)) : few;
 }
 
 extern "C" int tb_attn_paged(const tb_heads *q, const tb_heads *gate, const tb_kv_cache *cache, const int32_t *table, int width,

@@ -111,3 +111,17 @@ def test_either_kernel(rows, cache, requests, group, dim, kv):
     c.upload()
     guarded_run(c)
     c.check()
+
+
+def test_one_workspace_for_a_programs_steps():
+    """A workspace of the largest step serves the smaller ones, decodes and chunks."""
+    steps = [[(60, 1)] * 40, [(90, 30)], [(33, 3), (70, 1)], [(50, 1)]]
+    sized = False
+    for requests in steps:
+        c = Case(requests, 16, 2, 64, 16, "bf16", "bf16", seed=len(requests)).upload()
+        if not sized:
+            ws = Guarded(torch.zeros(tb.tb_attn_paged_workspace_bytes(c.handle, 16, torch.bfloat16, 40, 40), dtype=torch.uint8, device=gu.DEV))
+            sized = True
+        c.ws = ws.t
+        c.run().check()
+        assert ws.whole()
