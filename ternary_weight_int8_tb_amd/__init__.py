@@ -392,6 +392,13 @@ def _bad(fn: str, why: str):
     raise TbError(fn, TB_EINVAL, why)
 
 
+def _int32(fn: str, name: str, v: int) -> int:
+    """v, refused where 32 bits do not hold it: ctypes would cut it off."""
+    if not -1 << 31 <= v < 1 << 31:
+        _bad(fn, f"{name} = {v}")
+    return v
+
+
 _DTYPES: dict = {}
 
 
@@ -612,7 +619,7 @@ def tb_moe_combine(y, weights, ids, experts: int, out, stream=None) -> None:
     code, n, dev = _dtype(fn, out), int(out.shape[-1]), ids.device
     _check(fn, dev, ("y", y, torch.float32, (t * topk, n)), ("weights", weights, torch.float32, (t, topk)),
            ("ids", ids, torch.int32, (t, topk)), ("out", out, out.dtype, (t, n)))
-    _launch(fn, dev, stream, y.data_ptr(), weights.data_ptr(), ids.data_ptr(), t, topk, experts, n, out.data_ptr(), code)
+    _launch(fn, dev, stream, y.data_ptr(), weights.data_ptr(), ids.data_ptr(), t, topk, _int32(fn, "experts", experts), n, out.data_ptr(), code)
 
 
 # ---- attention over a paged cache ---------------------------------------------------------
@@ -640,7 +647,7 @@ class Rope:
         if freq.dim() != 1 or not freq.is_cuda:
             _bad(fn, "freq has to be a float64 vector on the GPU")
         _check(fn, freq.device, ("freq", freq, _torch().float64, freq.shape))
-        self.freq, self.device, self.rot, self.layout, self.factor = freq, freq.device, 2 * int(freq.shape[0]), int(layout), float(factor)
+        self.freq, self.device, self.rot, self.layout, self.factor = freq, freq.device, 2 * int(freq.shape[0]), _int32(fn, "layout", int(layout)), float(factor)
         self.c = CRope(freq.data_ptr(), self.rot, self.layout, self.factor)
         self.ref = ctypes.byref(self.c)
 
@@ -704,7 +711,7 @@ def tb_kv_plan(context, fresh, page: int, pages: int, table, free_list, count, l
            ("free_list", free_list, i32, (pages,)), ("count", count, i32, (1,)), ("lengths", lengths, i32, (n,)),
            ("offsets", offsets, i32, (n + 1,)), ("positions", positions, i32, (rows,)), ("slots", slots, i32, (rows,)),
            ("left", left, i32, (1,)), ("missing", missing, i32, (1,)))
-    _launch(fn, dev, stream, context.data_ptr(), fresh.data_ptr(), n, rows, page, pages, table.data_ptr(), width, free_list.data_ptr(),
+    _launch(fn, dev, stream, context.data_ptr(), fresh.data_ptr(), n, rows, _int32(fn, "page", page), pages, table.data_ptr(), width, free_list.data_ptr(),
             count.data_ptr(), lengths.data_ptr(), offsets.data_ptr(), positions.data_ptr(), slots.data_ptr(), left.data_ptr(),
             missing.data_ptr())
 
@@ -743,7 +750,8 @@ def tb_attn_paged_workspace_bytes(cache: KvCache, heads: int, dtype, requests: i
     """Bytes of device workspace tb_attn_paged needs for q rows of a torch dtype, with at most these requests and tokens."""
     torch = _torch()
     code = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.float16: TB_F16}.get(dtype, -1)
-    return int(lib().tb_attn_paged_workspace_bytes(cache.ref, int(heads), code, int(requests), int(tokens)))
+    sizes = (int(heads), code, int(requests), int(tokens))
+    return int(lib().tb_attn_paged_workspace_bytes(cache.ref, *sizes)) if max(sizes) < 1 << 31 else 0
 
 
 def tb_attn_paged(q, cache: KvCache, table, offsets, lengths, scale: float, out, ws, gate=None, window: int = 0, stream=None) -> None:
@@ -767,4 +775,4 @@ def tb_attn_paged(q, cache: KvCache, table, offsets, lengths, scale: float, out,
     if gate is not None:
         hg = ctypes.byref(_heads(fn, "gate", gate, dev, t, dim))
     _launch(fn, dev, stream, ctypes.byref(hq), hg, cache.ref, table.data_ptr(), width, offsets.data_ptr(), lengths.data_ptr(), n, t, scale,
-            window, out.data_ptr(), ws.data_ptr(), ws.numel())
+            _int32(fn, "window", window), out.data_ptr(), ws.data_ptr(), ws.numel())

@@ -9,7 +9,7 @@ import torch
 
 import ternary_weight_int8_tb_amd as tb
 from tests import gpu_util as gu
-from tests.test_gpu_attn_paged import KINDS, TYPES, Case, ints
+from tests.test_gpu_attn_paged import KINDS, Case, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +125,25 @@ def test_one_workspace_for_a_programs_steps():
         c.ws = ws.t
         c.run().check()
         assert ws.whole()
+
+
+def test_whole_numbers_past_32_bits():
+    """A window, a page size or a number of experts that 32 bits do not hold is refused, not cut off."""
+    c = Case([(40, 4)], 4, 2, 64, 16, "bf16", "bf16", seed=14).upload()
+    n = 2 ** 32
+    refused = [lambda: tb.tb_attn_paged(c.dq, c.handle, c.dt, c.do, c.dl, c.scale, c.out, c.ws, window=n),
+               lambda: tb.tb_attn_paged(c.dq, c.handle, c.dt, c.do, c.dl, c.scale, c.out, c.ws, window=n + 5),
+               lambda: tb.Rope(torch.zeros(32, dtype=torch.float64, device=gu.DEV), layout=n + 1)]
+    one, two = ints([1]), ints([0, 0])
+    table, rows = torch.zeros(1, 4, dtype=torch.int32, device=gu.DEV), torch.zeros(1, dtype=torch.int32, device=gu.DEV)
+    refused.append(lambda: tb.tb_kv_plan(ints([0]), ints([1]), n + 16, 8, table, ints(np.arange(8)), ints([8]), ints([0]), two, rows, rows.clone(),
+                                         ints([0]), ints([0])))
+    y = torch.zeros(2, 128, device=gu.DEV)
+    refused.append(lambda: tb.tb_moe_combine(y, torch.ones(1, 2, device=gu.DEV), torch.zeros(1, 2, dtype=torch.int32, device=gu.DEV), n + 4,
+                                             torch.zeros(1, 128, device=gu.DEV)))
+    for call in refused:
+        with pytest.raises(tb.TbError) as e:
+            call()
+        assert e.value.status == tb.TB_EINVAL
+    assert tb.tb_attn_paged_workspace_bytes(c.handle, 4, torch.bfloat16, n + 1, n + 4) == 0
+    assert torch.all(c.out == 77.0)

@@ -57,3 +57,12 @@ def test_workspace_is_enough(L):
         far = dict(zip(ATTN, [(i + 2) << 40 for i in range(5)]))
         assert call(q=heads(1 << 40), c=cache(k=8 << 40, v=9 << 40), requests=requests, tokens=tokens, ws_bytes=4096, **far) == tb.TB_EINVAL
         assert size > 4096
+
+
+def test_whole_numbers():
+    """Arguments that 32 bits do not hold are refused; ctypes would cut them off (a window of 2^32 would be none)."""
+    assert tb._int32("f", "n", 2 ** 31 - 1) == 2 ** 31 - 1 and tb._int32("f", "n", -2 ** 31) == -2 ** 31
+    for v in (2 ** 31, 2 ** 32, 2 ** 32 + 16, -2 ** 31 - 1):
+        with pytest.raises(tb.TbError) as e:
+            tb._int32("f", "n", v)
+        assert e.value.status == tb.TB_EINVAL
