@@ -533,6 +533,10 @@ typedef struct tb_heads {
  *   offsets   int32 [requests + 1], positions, slots int32 [rows] outputs
  *   left      int32 [1] output: entries of the free list afterwards; may be count itself
  *   missing   int32 [1] output: rows of requests that have no slot (0 unless pages or width ran out)
+ * After a step with missing > 0 its requests lack keys, and a later step does not take the pages that were not there: it
+ * counts those of the whole context as held. The caller puts the length of each such request back to the position of its first
+ * row without a slot, and brings the tokens from there on again; the pages that it did get stay its own. (Or it ends the request:
+ * the entries that name no page are passed over.)
  * requests, rows, width >= 1. TB_EUNSUPPORTED unless requests <= 16384, rows < 2^30,
  * requests * width < 2^30 and width * page <= 2^30; a context longer than 2^30 counts as that. */
 int tb_kv_plan(const int32_t *context, const int32_t *fresh, int requests, int rows, int page, int pages,

@@ -700,7 +700,8 @@ def tb_kv_plan(context, fresh, page: int, pages: int, table, free_list, count, l
 
     context, fresh [requests] (fresh -1: the request has ended), table [requests][width] and free_list [pages] updated,
     count [1] -> lengths [requests] (may be context), offsets [requests + 1], positions, slots [rows], left [1] (may be
-    count), missing [1]."""
+    count), missing [1]. Where missing > 0, put a request's length back to the position of its first row with slot -1, and
+    bring the tokens from there on again when there are pages."""
     fn = "tb_kv_plan"
     n, width = _matrix_rows(fn, "table", table)
     dev, i32 = table.device, _torch().int32
