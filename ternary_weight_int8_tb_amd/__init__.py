@@ -661,7 +661,11 @@ class Rope:
         "linear"  every pair is slowed by stretch
         "base"    the base is raised, so that the slowest pair is slowed by stretch and the fastest is kept
         "parts"   pairs that turn less than `slow` times over the trained length are slowed by stretch, those that turn more
-                  than `fast` times are kept, those between are mixed in proportion; factor = 0.1 ln(stretch) + 1"""
+                  than `fast` times are kept, those between are mixed in proportion to their turns; factor = 0.1 ln(stretch) + 1
+
+        A checkpoint may want another rule: pairs mixed in proportion to their index between the two bounds (the middle pair of
+        128 elements then differs by a factor of 1.7 at base 1e6 and stretch 4), or a factor of 1. Its frequencies and factor go
+        to Rope(freq, layout, factor) as they are."""
         import math
         import torch
         fn = "Rope.frequencies"
