@@ -147,3 +147,39 @@ def test_whole_numbers_past_32_bits():
         assert e.value.status == tb.TB_EINVAL
     assert tb.tb_attn_paged_workspace_bytes(c.handle, 4, torch.bfloat16, n + 1, n + 4) == 0
     assert torch.all(c.out == 77.0)
+
+
+@pytest.mark.parametrize("rows,cache", [("f32", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("dim,requests", [(256, [(20000, 1)]), (128, [(40000, 1)]), (64, [(70000, 1)]),
+                                          (256, [(30, 1)] * 9 + [(20000, 1)] + [(17, 1)] * 10), (128, [(9, 1)] * 40 + [(9000, 1)])])
+def test_units_of_hundreds_of_parts(rows, cache, dim, requests):
+    """A unit's parts in more trips of the join than one; the last third of the keys has values of its own, so that no part
+    can be left out."""
+    print(f"parts dim={dim} {[n for n, _ in requests if n > 99]} {rows}/{cache}", flush=True)
+    c = Case(requests, 2, 1, dim, 64, rows, cache, seed=dim)
+    s = max(range(len(requests)), key=lambda r: requests[r][0])
+    held = -(-c.lengths[s] // 64)
+    third = c.table[s, 2 * held // 3:held - 1]
+    c.v[third] += 3.0
+    c.k[third] *= 0.5
+    c.upload()
+    guarded_run(c)
+    c.check()
+
+
+@pytest.mark.parametrize("rows,cache", KINDS)
+@pytest.mark.parametrize("n,dim", [(300, 64), (700, 64), (300, 128), (600, 256)])
+def test_many_ragged_requests_of_several_tokens(n, dim, rows, cache):
+    """The kernel for many rows with hundreds of requests, some of them empty: each workgroup finds its own among them."""
+    print(f"many ragged {n} dim={dim} {rows}/{cache}", flush=True)
+    rng = np.random.default_rng(n + dim)
+    new = rng.choice([0, 0, 1, 2, 5, 9], n)
+    requests = [(int(m + x) if m else int(x), int(m)) for m, x in zip(new, rng.integers(0, 25, n))]
+    requests[n // 3] = (333, 130)
+    requests[n - 1] = (0, 0)
+    assert sum(m for _, m in requests) > n + 128
+    c = Case(requests, 2, 2, dim, 16, rows, cache, seed=n)
+    c.upload(extra=1)
+    guarded_run(c)
+    c.check()
+    assert torch.all(c.out[c.tokens:] == 77.0)
