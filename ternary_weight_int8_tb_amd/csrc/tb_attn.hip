@@ -867,7 +867,7 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int slot, bool begi
 // A wave takes every fourth block of 32 keys, through buffers of its own: no barriers, and a wave's next keys are
 // on their way while it multiplies its values, and the other way round.
 // Bound: memory, behind a chain of latencies. One fp32 token of 16 heads over 131072 keys of 2 x 256 bf16: the loops
-// read 268 MB in 38 us, 7 TB/s; 9 us before them (the line of units 1.5, pages and q 2.8, the first keys) and 4 after; the
+// read 268 MB in 38 us, 7 TB/s (some of it from the last cache: memory alone gives 5.9); 9 us before them (the line of units 1.5, pages and q 2.8, the first keys) and 4 after; the
 // join 8. The same over 4096 keys: 15 us, of which no part is over 2, and 7.
 constexpr int kNarrowWaves = 4, kNarrowRows = 16, kNarrowStep = kNarrowWaves * kBlk;
 constexpr int kNarrowExtra = 2;   // in steps: 48 ragged requests, 0: 71 us, 2: 47
@@ -1100,10 +1100,11 @@ __global__ __launch_bounds__(kNarrowWaves * 64, narrow_per_cu(D)) void attn_narr
 //   them in two workgroups a CU, the same number of cycles, but twice the loads, and a lower clock (357 us against 333).
 //   D = 128: two workgroups a CU, 32 keys a step and four buffers (a mixed step of 12 requests: 73 us; 64 keys and two
 //   buffers 75; eight waves that share 64 keys 77; three workgroups a CU the same as two).
-// Bound: the power limit and the loop's waits. 2048 new bf16 tokens behind 8192, 16 heads of 256: 303 to 325 us with the join,
-// 0.95 to 1.02 PFLOP/s, at 1.8 to 2.0 GHz; the matrix cores are busy in 47% of the cycles, and vector operations take another
-// 30%. A library product of 8192^3 reaches 1.19 to 1.26.
-// wide_extra: what beginning and ending a unit takes, in steps (q and the first keys 6 us, rows out 4 to 11).
+// Bound: the loop's waits. 2048 new bf16 tokens behind 8192, 16 heads of 256: 301 to 325 us with the join, 0.95 to 1.03
+// PFLOP/s; under counters, at 1.9 GHz, the matrix cores are busy in 47% of the cycles, and vector operations take another 30%. A
+// library product of 8192^3 reaches 1.19 to 1.26. Rows in fp32, three products for one: 680 to 716. 16 heads on 4 x 64: 132.
+// wide_extra: what beginning and ending a unit takes, in steps. D = 256: q and the first keys 6 us, rows out 4 to 11; D = 128, 12
+// requests with chunks of up to 509: 3 and 5, beside 1.5 a step.
 constexpr int wide_extra(int dim) { return dim == 256 ? 6 : 8; }
 constexpr int wide_step(int dim) { return dim == 256 ? 64 : 32; }     // keys
 constexpr int wide_buffers(int dim) { return dim == 256 ? 2 : 4; }

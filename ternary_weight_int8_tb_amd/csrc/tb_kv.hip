@@ -14,11 +14,12 @@ using namespace tbr;
 // ------------------------------------------------------------------------------------
 // The plan: one workgroup. Its parts depend on one another (rows cut at the step's, pages
 // pushed before they are popped, slots read from the table's new entries), each is a scan over the
-// requests or a few entries a thread, and a second launch costs more than they do.
+// requests or a few entries a thread, and up to hundreds of requests a second launch costs more than they do.
 // Pages taken and rows of the step are dealt to the threads, not requests: their numbers differ by
 // request from none to hundreds. A thread finds its request by a search in the scan, in LDS.
 // Bound: latency, of some twenty dependent accesses. 1 request 5 us; 250 requests, 2048 rows 11; 2048 requests, 16384
-// rows 28. (Four entries a thread with their loads in flight together: 8, 13 and 29.)
+// rows 28, most of which are the rows' lengths and table entries, read one behind the other, four rows a thread: positions and slots
+// in a second launch over all CUs might take less there; not tried. (Four entries a thread with their loads in flight together: 8, 13 and 29.)
 // ------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxRequests = 16384;
