@@ -585,7 +585,8 @@ int tb_rope_kv(const tb_heads *q, const tb_heads *k, const tb_heads *v, int toke
  * weights of the softmax are rounded to it; of fp32 rows q and the weights are split into parts whose sum has
  * 22 bits (fp16) or 24 (bf16). With an fp16 cache the smallest have fewer: weights below 2^-15 of the row's largest are
  * off by up to 2^-38 of that, elements of q below 2^-11 of the row's largest by up to 2^-34 of that; weights of fp16 rows
- * below 2^-20 of the largest by up to 2^-31 of that.
+ * below 2^-20 of the largest by up to 2^-31 of that. With a bf16 cache sums over up to 2^20 keys of any values are
+ * numbers; parts of a result below 2^-121 are lost.
  * Where tokens > requests the call is made for chunks, else for single tokens of each request. A prompt among as many requests
  * that wait takes longer than by itself: its time is best with the waiting ones left out of the call.
  * The order of the sums, and so a row's low-order bits, depend on the lengths of all requests of the call;

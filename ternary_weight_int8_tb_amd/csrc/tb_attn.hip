@@ -429,13 +429,13 @@ struct Rows {
     static constexpr int kQ = D / 32, kO = D / 16, kParts = Split<T, EXACT>::kParts;
     // Weights start at 2^kBias (of fp32 rows at kUnit, a factor: in the exponent it would cost bits), and a row's maximum lags by a
     // factor of 2^kLag at most.
-    // bf16: so far below one that sums of the largest values that the cache holds are fp32 numbers. (2^30 keys of weights up to
-    // 2^-32; weights that fp32 has no more are 2^-86 of the largest.)
+    // bf16: so far below one that sums of the largest values that the cache holds are fp32 numbers (of 2^20 keys, with weights up
+    // to 2^-20), and no further, as fp32 ends at 2^-149: values down to 2^-110 keep their 8 bits under the largest weight.
     // fp16: so far above one that small weights keep their bits, and the largest, 2^14 or 2^15, still fits. Of fp32 rows a weight's
     // second part must keep its bits too. Its last one is 2^-24: both parts are off by 2^-25 at most, 2^-38 of the largest weight, and
     // the sum of 22 bits is whole from 2^-15 of that on. (At 2^6 weights of e^-16 would be off by up to 2^-8 of themselves.)
     static constexpr bool kFine = EXACT && std::is_same<T, F16>::value;
-    static constexpr float kBias = std::is_same<T, F16>::value ? 6.0f : -40.0f, kUnit = kFine ? 0x1p13f : 0x1p-40f;
+    static constexpr float kBias = std::is_same<T, F16>::value ? 6.0f : -28.0f, kUnit = kFine ? 0x1p13f : 0x1p-28f;
     static constexpr float kLag = kFine ? 2.0f : 8.0f;
     uint4 q[NT][kQ][kParts];
     v4f o[NT][kO];

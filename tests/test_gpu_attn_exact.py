@@ -184,3 +184,22 @@ def test_tiny_and_large_scales(rows, cache):
             want = v[:seen, 0].mean() if alike else v[best, 0]
             # whole numbers: their sums are exact
             assert np.all(np.abs(got[i] - want) <= (HALF_STEP[rows] + 8 * U) * abs(want)), (scale, i, got[i, 0, 0], want)
+
+
+@pytest.mark.parametrize("rows", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [2.0 ** -110, 2.0 ** -97, 1.5 * 2.0 ** 127])
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 3), (256, 1), (256, 60)])
+def test_values_of_any_magnitude(rows, value, dim, new):
+    """Small bf16 values keep all their bits beside the room for large ones."""
+    print(f"values of {value:g} {rows} dim={dim} new={new}", flush=True)
+    n = 700
+    c = Case([(n, new)], 4, 2, dim, 16, rows, "bf16", seed=7)
+    x = (1 + np.arange(n) % 64 / 128)[:, None] + np.zeros((n, dim))
+    if value > 1:
+        x[:] = 1.0
+    fill(c, [np.zeros((n, dim))], [x * value])
+    got = said(c.upload().run())
+    for i in range(new):
+        want = x[:n - new + i + 1, 0].mean() * value
+        # all weights are one: each product is exact, and so are the weights' sum and, up to 2^-149, that of the products
+        assert np.all(np.abs(got[i] / want - 1) <= (n + 20) * U + HALF_STEP[rows] * 1.001), (got[i, 0, 0], want)
